@@ -12,10 +12,15 @@ Entry points (same names as the C ABI):
 * :func:`fa_bwd` -- recompute backward pass, returns ``(dq, dk, dv)``;
 * :func:`fa_decode_splitkv` -- split-KV decode over a ragged packed KV cache,
   returns ``(o, lse)``;
+* :func:`fa_cache_write`, :func:`fa_cache_read` -- new keys and values into a paged
+  cache, in bf16 or in 8 bits, and a paged cache back into packed rows;
+* :func:`fa_fwd_paged` -- attention of a chunk of new tokens per sequence over a
+  paged cache, :func:`fa_decode_paged_q8` -- of single tokens over an 8 bit one;
 * :func:`fa_check` -- synchronise and read the kernels' status word.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -28,6 +33,7 @@ __all__ = [
     "fa_decode_splitkv_checked", "fa_decode_paged", "fa_merge_partials", "fa_fwd_shard", "fa_bwd_shard", "fa_check",
     "fa_fwd_workspace_size", "fa_bwd_workspace_size",
     "fa_bwd_varlen_workspace_size", "fa_decode_workspace_size", "fa_decode_num_splits",
+    "fa_cache_write", "fa_cache_read", "fa_fwd_paged", "fa_decode_paged_q8", "fa_paged_workspace_size",
     "fa_version", "STATUS",
 ]
 
@@ -83,6 +89,15 @@ def load():
         lib.fa_merge_partials.argtypes = [_vp, _vp] + [_i] * 5 + [_vp, _vp, _vp]
         lib.fa_fwd_shard.argtypes = [_vp] * 5 + [_i] * 7 + [_f, _vp, _sz, _vp]
         lib.fa_bwd_shard.argtypes = [_vp] * 9 + [_i] * 7 + [_f, _vp, _sz, _vp]
+        _ll = ctypes.c_longlong
+        lib.fa_cache_write.argtypes = [_vp] * 2 + [_ll] * 2 + [_vp] * 7 + [_i] * 7 + [_vp, _sz, _vp]
+        lib.fa_cache_read.argtypes = [_vp] * 8 + [_i] * 7 + [_vp, _sz, _vp]
+        lib.fa_fwd_paged.argtypes = [_vp, _ll] + [_vp] * 9 + [_i] * 11 + [_f, _vp, _sz, _vp]
+        lib.fa_decode_paged_q8.argtypes = [_vp] * 7 + [_i] * 8 + [_f, _vp, _vp, _vp, _sz, _vp]
+        for fn in (lib.fa_cache_write, lib.fa_cache_read, lib.fa_fwd_paged, lib.fa_decode_paged_q8):
+            fn.restype = _i
+        lib.fa_paged_workspace_size.argtypes = [_i] * 6
+        lib.fa_paged_workspace_size.restype = _sz
         for fn in (lib.fa_fwd, lib.fa_bwd, lib.fa_decode_splitkv, lib.fa_decode_splitkv_noalloc,
                    lib.fa_decode_splitkv_checked, lib.fa_decode_paged, lib.fa_fwd_varlen, lib.fa_bwd_varlen,
                    lib.fa_fwd_masked, lib.fa_bwd_masked, lib.fa_fwd_blocksparse, lib.fa_bwd_blocksparse,
@@ -134,6 +149,10 @@ def fa_decode_num_splits(B, H, max_seqlen_k, d, num_splits=0) -> int:
     return int(load().fa_decode_num_splits(B, H, max_seqlen_k, d, num_splits))
 
 
+def fa_paged_workspace_size(B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d) -> int:
+    return int(load().fa_paged_workspace_size(B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d))
+
+
 # --------------------------------------------------------------------------- workspaces
 
 _ws_cache: dict = {}
@@ -151,6 +170,28 @@ def workspace(nbytes: int, device, tag: str = "default") -> torch.Tensor:
         ws = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
         _ws_cache[key] = ws
     return ws
+
+
+_paged_bytes = 0
+
+
+def paged_workspace(device=None, nbytes: int = 0) -> torch.Tensor:
+    """The workspace that the paged cache calls use on the current stream of `device`
+    when they are given none; pass it to :func:`fa_check` after them.
+
+    One per stream, since two calls that may run at the same time must not share a
+    workspace.  Calls under stream capture get one of their own from the graph's
+    memory, so that graphs share it neither with each other nor with eager calls."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    global _paged_bytes
+    if not _paged_bytes:  # one call of few rows: what most calls need
+        _paged_bytes = fa_paged_workspace_size(1, 1, 1, 1, 1, 128)
+    nbytes = max(int(nbytes), _paged_bytes)
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws[:256].zero_()  # the status word; the rest is written before it is read
+        return ws
+    return workspace(nbytes, dev, f"paged:{_stream_ptr(dev)}")
 
 
 def _stream_ptr(device) -> int:
@@ -557,6 +598,183 @@ def fa_decode_paged(q, k_pages, v_pages, block_table, seqlens_k, max_seqlen_k: i
                              int(max_seqlen_k), d, _scale(softmax_scale), int(num_splits), out.data_ptr(),
                              lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr(q.device))
     _raise("fa_decode_paged", st)
+    return out, lse
+
+
+# --------------------------------------------------------------------------- paged cache
+
+
+def _on_device(t):
+    """Launches go to the current device: make it the tensor's for the call."""
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _check_rows(name, t, H, d):
+    """Packed rows [total, H, d] bf16 whose rows may be further apart than H d (a slice
+    of a fused projection).  Returns elements between rows."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != d:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [total, {H}, {d}]")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (H > 1 and s1 != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return H * d if t.shape[0] == 1 else s0
+
+
+def _check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B, d=None):
+    """Checks a paged cache; returns (num_pages, page_size, H, d, k_scales pointer, v_scales pointer)."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages/v_pages must be [num_pages, page_size, H, d]")
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales and v_scales are given together or not at all")
+    dtype = torch.bfloat16 if k_scales is None else torch.float8_e4m3fn
+    shape = tuple(k_pages.shape)
+    _check_tensor("k_pages", k_pages, dtype)
+    _check_tensor("v_pages", v_pages, dtype, shape)
+    ks = vs = None
+    if k_scales is not None:
+        _check_tensor("k_scales", k_scales, torch.uint8, shape[:3])
+        _check_tensor("v_scales", v_scales, torch.uint8, shape[:3])
+        ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages_per_seq]")
+    _check_tensor("block_table", block_table, torch.int32)
+    if d is not None and shape[3] != d:
+        raise ValueError(f"the pages' head dimension is {shape[3]}, expected {d}")
+    return shape + (ks, vs)
+
+
+def _same_device(t, *others):
+    for x in others:
+        if x is not None and x.device != t.device:
+            raise ValueError(f"tensors on {t.device} and {x.device}")
+
+
+def fa_cache_write(k, v, k_pages, v_pages, cu_seqlens, block_table, seqlens_k, k_scales=None, v_scales=None,
+                   ws=None) -> None:
+    """Write new keys and values into a paged cache.  k, v [total, H, d] bf16 (rows may
+    be strided), sequence b's new rows cu_seqlens[b] .. cu_seqlens[b+1]-1 going to its
+    last positions, seqlens_k[b] - n_b .. seqlens_k[b] - 1.  Pages bf16, or
+    torch.float8_e4m3fn with scale bytes k_scales, v_scales [num_pages, page_size, H]
+    (uint8): a row's slice of one head stands for codes * 2^(byte - 127)."""
+    lib = load()
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1:
+        raise ValueError("cu_seqlens must be [B+1]")
+    B = cu_seqlens.shape[0] - 1
+    P, page, H, d, ks, vs = _check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B)
+    k_stride, v_stride = _check_rows("k", k, H, d), _check_rows("v", v, H, d)
+    if v.shape != k.shape:
+        raise ValueError("k and v differ in shape")
+    _check_tensor("cu_seqlens", cu_seqlens, torch.int32)
+    _check_tensor("seqlens_k", seqlens_k, torch.int32, (B,))
+    _same_device(k, v, k_pages, v_pages, cu_seqlens, block_table, seqlens_k, k_scales, v_scales, ws)
+    with _on_device(k):
+        if ws is None:
+            ws = paged_workspace(k.device)
+        st = lib.fa_cache_write(k.data_ptr(), v.data_ptr(), k_stride, v_stride, cu_seqlens.data_ptr(),
+                                block_table.data_ptr(), seqlens_k.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                ks, vs, B, H, k.shape[0], P, page, block_table.shape[1], d, ws.data_ptr(),
+                                ws.numel(), _stream_ptr(k.device))
+    _raise("fa_cache_write", st)
+
+
+def fa_cache_read(k_pages, v_pages, cu_seqlens_k, block_table, total_k: int, k_scales=None, v_scales=None,
+                  out_k=None, out_v=None, ws=None):
+    """Read sequences back from a paged cache: keys 0 .. n_b - 1 of sequence b, n_b =
+    cu_seqlens_k[b+1] - cu_seqlens_k[b], into rows cu_seqlens_k[b] .. of (k, v)
+    [total_k, H, d] bf16, exactly.  Rows that belong to no sequence are left alone."""
+    lib = load()
+    if not isinstance(cu_seqlens_k, torch.Tensor) or cu_seqlens_k.dim() != 1:
+        raise ValueError("cu_seqlens_k must be [B+1]")
+    B = cu_seqlens_k.shape[0] - 1
+    P, page, H, d, ks, vs = _check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B)
+    total_k = int(total_k)
+    _check_tensor("cu_seqlens_k", cu_seqlens_k, torch.int32)
+    out_k = torch.empty((total_k, H, d), dtype=torch.bfloat16, device=k_pages.device) if out_k is None else out_k
+    out_v = torch.empty((total_k, H, d), dtype=torch.bfloat16, device=k_pages.device) if out_v is None else out_v
+    _check_tensor("out_k", out_k, torch.bfloat16, (total_k, H, d))
+    _check_tensor("out_v", out_v, torch.bfloat16, (total_k, H, d))
+    _same_device(k_pages, v_pages, cu_seqlens_k, block_table, k_scales, v_scales, out_k, out_v, ws)
+    with _on_device(k_pages):
+        if ws is None:
+            ws = paged_workspace(k_pages.device)
+        st = lib.fa_cache_read(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, cu_seqlens_k.data_ptr(),
+                               block_table.data_ptr(), out_k.data_ptr(), out_v.data_ptr(), B, H, total_k, P, page,
+                               block_table.shape[1], d, ws.data_ptr(), ws.numel(), _stream_ptr(k_pages.device))
+    _raise("fa_cache_read", st)
+    return out_k, out_v
+
+
+def fa_fwd_paged(q, k_pages, v_pages, cu_seqlens_q, block_table, seqlens_k, max_seqlen_q: int, max_seqlen_k: int,
+                 causal: bool = False, softmax_scale=None, k_scales=None, v_scales=None, out=None, lse=None, ws=None):
+    """Attention of a chunk of new tokens per sequence over a paged cache that already
+    holds them.  q [total_q, Hq, d] bf16 (rows may be strided), sequence b's tokens
+    cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 being the last of its seqlens_k[b] keys;
+    pages [num_pages, page_size, Hkv, d], bf16 or 8 bit with scales (fa_cache_write);
+    query head h reads key head h // (Hq / Hkv).  Returns (o [total_q, Hq, d] bf16,
+    lse [Hq, total_q] fp32)."""
+    lib = load()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [total_q, Hq, d]")
+    total_q, Hq, d = q.shape
+    if not isinstance(cu_seqlens_q, torch.Tensor) or cu_seqlens_q.dim() != 1:
+        raise ValueError("cu_seqlens_q must be [B+1]")
+    B = cu_seqlens_q.shape[0] - 1
+    q_stride = _check_rows("q", q, Hq, d)
+    P, page, Hkv, _, ks, vs = _check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B, d)
+    _check_tensor("cu_seqlens_q", cu_seqlens_q, torch.int32)
+    _check_tensor("seqlens_k", seqlens_k, torch.int32, (B,))
+    out = torch.empty((total_q, Hq, d), dtype=torch.bfloat16, device=q.device) if out is None else out
+    lse = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device) if lse is None else lse
+    _check_tensor("out", out, torch.bfloat16, (total_q, Hq, d))
+    _check_tensor("lse", lse, torch.float32, (Hq, total_q))
+    _same_device(q, k_pages, v_pages, cu_seqlens_q, block_table, seqlens_k, k_scales, v_scales, out, lse, ws)
+    with _on_device(q):
+        if ws is None:
+            ws = paged_workspace(q.device, lib.fa_paged_workspace_size(B, Hq, Hkv, int(max_seqlen_q),
+                                                                       int(max_seqlen_k), d))
+        st = lib.fa_fwd_paged(q.data_ptr(), q_stride, k_pages.data_ptr(), v_pages.data_ptr(), ks, vs,
+                              cu_seqlens_q.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(), out.data_ptr(),
+                              lse.data_ptr(), B, Hq, Hkv, total_q, P, page, block_table.shape[1], int(max_seqlen_q),
+                              int(max_seqlen_k), d, int(bool(causal)), _scale(softmax_scale), ws.data_ptr(),
+                              ws.numel(), _stream_ptr(q.device))
+    _raise("fa_fwd_paged", st)
+    return out, lse
+
+
+def fa_decode_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, max_seqlen_k: int,
+                       softmax_scale=None, out=None, lse=None, ws=None):
+    """Single-token attention over an 8 bit paged cache.  q [B, Hq, d] bf16; pages
+    [num_pages, page_size, Hkv, d] torch.float8_e4m3fn with scale bytes [num_pages,
+    page_size, Hkv] (fa_cache_write); block_table int32 [B, max_pages_per_seq];
+    seqlens_k int32 [B].  Returns (o [B, Hq, d] bf16, lse [B, Hq] fp32)."""
+    lib = load()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [B, Hq, d]")
+    B, Hq, d = q.shape
+    _check_tensor("q", q, torch.bfloat16)
+    if k_scales is None:
+        raise ValueError("k_scales and v_scales are needed")
+    P, page, Hkv, _, ks, vs = _check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B, d)
+    _check_tensor("seqlens_k", seqlens_k, torch.int32, (B,))
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
+    _check_tensor("out", out, torch.bfloat16, (B, Hq, d))
+    _check_tensor("lse", lse, torch.float32, (B, Hq))
+    _same_device(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, out, lse, ws)
+    with _on_device(q):
+        if ws is None:
+            ws = paged_workspace(q.device, lib.fa_paged_workspace_size(B, Hq, Hkv, 1, int(max_seqlen_k), d))
+        st = lib.fa_decode_paged_q8(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ks, vs,
+                                    block_table.data_ptr(), seqlens_k.data_ptr(), B, Hq, Hkv, P, page,
+                                    block_table.shape[1], int(max_seqlen_k), d, _scale(softmax_scale),
+                                    out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr(q.device))
+    _raise("fa_decode_paged_q8", st)
     return out, lse
 
 

@@ -19,7 +19,8 @@ namespace fa {
 namespace {
 const char* const kKernelNames[kKCount] = {"fa_fwd_kernel", "fa_bwd_preprocess_kernel", "fa_bwd_main_kernel",
                                            "fa_bwd_convert_kernel", "fa_decode_kernel",
-                                           "fa_decode_check_kernel"};
+                                           "fa_decode_check_kernel", "fa_cache_write_kernel",
+                                           "fa_cache_read_kernel", "fa_paged_kernel", "fa_paged_merge_kernel"};
 struct ProfRecord {
   int kernel;
   cudaEvent_t start, stop;
@@ -125,6 +126,18 @@ bool encode_rows_map(CUtensorMap* map, const void* ptr, int rows, int H, int D, 
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool encode_matrix_map(CUtensorMap* map, const void* ptr, long long rows, int cols, bool bytes, int box_rows) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * (bytes ? 1 : 2)};
+  const cuuint32_t box[2] = {bytes ? 128u : 64u, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 unsigned long long wait_timeout_ns() {
@@ -583,6 +596,185 @@ fa_status fa_decode_paged(const void* q, const void* k_pages, const void* v_page
   a.check_args = 0;
   a.timeout_ns = wait_timeout_ns();
   return launch_decode(a, stream);
+}
+
+// Sizes and pointers that the paged cache calls share.  Rows of the flattened pages are
+// counted in 32 bits.
+static fa_status check_pages(const void* k_pages, const void* v_pages, const uint8_t* k_scales, const uint8_t* v_scales,
+                             const int32_t* block_table, int B, int H, int num_pages, int page_size, int max_pages,
+                             int d) {
+  if (!k_pages || !v_pages || !block_table || (k_scales == nullptr) != (v_scales == nullptr)) return FA_ERR_INVALID_ARG;
+  if (B <= 0 || H <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if ((long long)num_pages * page_size >= (1LL << 31) || (long long)max_pages * page_size >= (1LL << 31) ||
+      (long long)H * d >= (1LL << 20))
+    return FA_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || (reinterpret_cast<uintptr_t>(block_table) & 3u))
+    return FA_ERR_ALIGNMENT;
+  return FA_OK;
+}
+
+fa_status fa_cache_write(const void* k, const void* v, long long k_row_stride, long long v_row_stride,
+                         const int32_t* cu_seqlens, const int32_t* block_table, const int32_t* seqlens_k, void* k_pages,
+                         void* v_pages, uint8_t* k_scales, uint8_t* v_scales, int B, int H, int total, int num_pages,
+                         int page_size, int max_pages_per_seq, int d, void* workspace, size_t workspace_bytes,
+                         cudaStream_t stream) {
+  const NvtxRange range("fa_cache_write");
+  if (!k || !v || !cu_seqlens || !seqlens_k || total <= 0) return FA_ERR_INVALID_ARG;
+  const fa_status st = check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B, H, num_pages, page_size,
+                                   max_pages_per_seq, d);
+  if (st != FA_OK) return st;
+  if (k_row_stride < (long long)H * d || v_row_stride < (long long)H * d) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || k_row_stride % 8 || v_row_stride % 8 ||
+      (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u))
+    return FA_ERR_ALIGNMENT;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < kStatusBytes) return FA_ERR_WORKSPACE;
+  CacheLaunch a;
+  a.write = true;
+  a.q8 = k_scales != nullptr;
+  a.k = const_cast<void*>(k);
+  a.v = const_cast<void*>(v);
+  a.k_stride = k_row_stride;
+  a.v_stride = v_row_stride;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.cu = cu_seqlens;
+  a.seqlens = seqlens_k;
+  a.table = block_table;
+  a.status = static_cast<int*>(workspace);
+  a.B = B;
+  a.H = H;
+  a.d = d;
+  a.total = total;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  return launch_cache(a, stream);
+}
+
+fa_status fa_cache_read(const void* k_pages, const void* v_pages, const uint8_t* k_scales, const uint8_t* v_scales,
+                        const int32_t* cu_seqlens_k, const int32_t* block_table, void* k, void* v, int B, int H,
+                        int total_k, int num_pages, int page_size, int max_pages_per_seq, int d, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream) {
+  const NvtxRange range("fa_cache_read");
+  if (!k || !v || !cu_seqlens_k || total_k <= 0) return FA_ERR_INVALID_ARG;
+  const fa_status st = check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B, H, num_pages, page_size,
+                                   max_pages_per_seq, d);
+  if (st != FA_OK) return st;
+  if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(cu_seqlens_k) & 3u)) return FA_ERR_ALIGNMENT;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < kStatusBytes) return FA_ERR_WORKSPACE;
+  CacheLaunch a;
+  a.write = false;
+  a.q8 = k_scales != nullptr;
+  a.k = k;
+  a.v = v;
+  a.k_pages = const_cast<void*>(k_pages);
+  a.v_pages = const_cast<void*>(v_pages);
+  a.k_scales = const_cast<uint8_t*>(k_scales);
+  a.v_scales = const_cast<uint8_t*>(v_scales);
+  a.cu = cu_seqlens_k;
+  a.table = block_table;
+  a.status = static_cast<int*>(workspace);
+  a.B = B;
+  a.H = H;
+  a.d = d;
+  a.total = total_k;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  return launch_cache(a, stream);
+}
+
+// Head counts and lengths that the paged attention calls share.
+static bool paged_sizes_ok(int B, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_seqlen_q <= 0 || max_seqlen_k < 0) return false;
+  // rows of a chunk, and one sequence's 128-key tiles times its row tiles, in 32 bits
+  const long long rows = (long long)max_seqlen_q * (Hq / Hkv);
+  return rows < (1LL << 31) &&
+         (rows / 32 + 1) * Hkv < (1LL << 31) / ((long long)max_seqlen_k / 128 + 1) && Hq < (1 << 16);
+}
+
+size_t fa_paged_workspace_size(int B, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int d) {
+  if (!paged_sizes_ok(B, Hq, Hkv, max_seqlen_q, max_seqlen_k) || (d != 64 && d != 128)) return 0;
+  return paged_workspace_bytes();
+}
+
+static fa_status fwd_paged(const void* q, long long q_row_stride, const void* k_pages, const void* v_pages,
+                           const uint8_t* k_scales, const uint8_t* v_scales, const int32_t* cu_seqlens_q,
+                           const int32_t* block_table, const int32_t* seqlens_k, void* o, float* lse, int B, int Hq,
+                           int Hkv, int total_q, int num_pages, int page_size, int max_pages, int max_seqlen_q,
+                           int max_seqlen_k, int d, int causal, float softmax_scale, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+  if (!q || !seqlens_k || !o || !lse || total_q <= 0) return FA_ERR_INVALID_ARG;
+  const fa_status st =
+      check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B, Hkv, num_pages, page_size, max_pages, d);
+  if (st != FA_OK) return st;
+  if (!paged_sizes_ok(B, Hq, Hkv, max_seqlen_q, max_seqlen_k) || (long long)total_q * Hq >= (1LL << 31))
+    return FA_ERR_INVALID_ARG;
+  // every key a sequence may hold must have a block-table entry
+  if ((long long)max_seqlen_k > (long long)max_pages * page_size) return FA_ERR_INVALID_ARG;
+  if (q_row_stride < (long long)Hq * d) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || q_row_stride % 8 || !aligned16(o) || !aligned16(lse) ||
+      (reinterpret_cast<uintptr_t>(cu_seqlens_q) & 3u) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u))
+    return FA_ERR_ALIGNMENT;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < paged_workspace_bytes()) return FA_ERR_WORKSPACE;
+  PagedLaunch a;
+  a.q = q;
+  a.q_stride = q_row_stride;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.cu_q = cu_seqlens_q;
+  a.table = block_table;
+  a.seqlens = seqlens_k;
+  a.o = o;
+  a.lse = lse;
+  // packed: lse [Hq, total_q]; one token per sequence: lse [B, Hq]
+  a.lse_head = cu_seqlens_q ? total_q : 1;
+  a.lse_row = cu_seqlens_q ? 1 : Hq;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.total_q = total_q;
+  a.max_q = max_seqlen_q;
+  a.max_k = max_seqlen_k;
+  a.d = d;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.causal = causal ? 1 : 0;
+  a.scale = resolve_scale(softmax_scale, d);
+  a.workspace = workspace;
+  a.timeout_ns = wait_timeout_ns();
+  return launch_paged(a, stream);
+}
+
+fa_status fa_fwd_paged(const void* q, long long q_row_stride, const void* k_pages, const void* v_pages,
+                       const uint8_t* k_scales, const uint8_t* v_scales, const int32_t* cu_seqlens_q,
+                       const int32_t* block_table, const int32_t* seqlens_k, void* o, float* lse, int B, int Hq,
+                       int Hkv, int total_q, int num_pages, int page_size, int max_pages_per_seq, int max_seqlen_q,
+                       int max_seqlen_k, int d, int causal, float softmax_scale, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream) {
+  const NvtxRange range("fa_fwd_paged");
+  if (!cu_seqlens_q) return FA_ERR_INVALID_ARG;
+  return fwd_paged(q, q_row_stride, k_pages, v_pages, k_scales, v_scales, cu_seqlens_q, block_table, seqlens_k, o, lse,
+                   B, Hq, Hkv, total_q, num_pages, page_size, max_pages_per_seq, max_seqlen_q, max_seqlen_k, d, causal,
+                   softmax_scale, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_decode_paged_q8(const void* q, const void* k_pages, const void* v_pages, const uint8_t* k_scales,
+                             const uint8_t* v_scales, const int32_t* block_table, const int32_t* seqlens_k, int B,
+                             int Hq, int Hkv, int num_pages, int page_size, int max_pages_per_seq, int max_seqlen_k,
+                             int d, float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
+  const NvtxRange range("fa_decode_paged_q8");
+  if (!k_scales || !v_scales) return FA_ERR_INVALID_ARG;
+  return fwd_paged(q, (long long)Hq * d, k_pages, v_pages, k_scales, v_scales, nullptr, block_table, seqlens_k, o, lse,
+                   B, Hq, Hkv, B, num_pages, page_size, max_pages_per_seq, 1, max_seqlen_k, d, 0, softmax_scale,
+                   workspace, workspace_bytes, stream);
 }
 
 fa_status fa_profile_start(void) {

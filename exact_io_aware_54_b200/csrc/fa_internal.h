@@ -45,7 +45,8 @@ constexpr int kStatusTimeout = 6;
 constexpr int kStatusBadArg = 1;
 
 // Kernels the library launches (for the optional launch profiler).
-enum KernelId { kKFwd = 0, kKBwdPre, kKBwdMain, kKBwdConvert, kKDecode, kKDecodeCheck, kKCount };
+enum KernelId { kKFwd = 0, kKBwdPre, kKBwdMain, kKBwdConvert, kKDecode, kKDecodeCheck, kKCacheWrite,
+                kKCacheRead, kKPaged, kKPagedMerge, kKCount };
 // Bracket a launch with profiling events when profiling is on (no-ops otherwise).
 void prof_before(cudaStream_t s, int kernel_id);
 void prof_after(cudaStream_t s, int kernel_id);
@@ -95,7 +96,9 @@ bool encode_bshd_map(CUtensorMap* map, const void* ptr, int B, int N, int H, int
 // box_rows rows, 128-byte swizzled (zeros outside the tensor).
 bool encode_rows_map(CUtensorMap* map, const void* ptr, int rows, int H, int D, int box_rows);
 
-// The same for an fp32 tensor [B, N, H, D]: box of 128 rows x 32 columns (128 bytes), 128-byte swizzle.
+// Map of a row-major [rows, cols] tensor of bytes (bytes = true) or bf16, boxes of 128
+// bytes x box_rows rows, 128-byte swizzled (zeros outside the tensor).
+bool encode_matrix_map(CUtensorMap* map, const void* ptr, long long rows, int cols, bool bytes, int box_rows);
 
 struct FwdLaunch {
   const void* q;
@@ -201,6 +204,48 @@ struct DecodeLaunch {
   unsigned long long timeout_ns;
 };
 fa_status launch_decode(const DecodeLaunch& a, cudaStream_t stream);
+
+// Writing packed rows into a paged cache, or reading them back (cache_sm100.cu).  Pages
+// are [num_pages, page_size, H, d], bf16 or (q8) e4m3 codes with scale bytes
+// [num_pages, page_size, H].
+struct CacheLaunch {
+  bool write, q8;
+  void* k;  // packed rows [total, H, d] bf16 (written by a read)
+  void* v;
+  long long k_stride = 0, v_stride = 0;  // write: elements between rows
+  void* k_pages;
+  void* v_pages;
+  uint8_t* k_scales = nullptr;
+  uint8_t* v_scales = nullptr;
+  const int32_t* cu;
+  const int32_t* seqlens = nullptr;  // write: keys per sequence after it
+  const int32_t* table;
+  int* status;
+  int B, H, d, total, num_pages, page_size, max_pages;
+};
+fa_status launch_cache(const CacheLaunch& a, cudaStream_t stream);
+
+// Attention of new tokens over a paged cache (paged_sm100.cu).
+struct PagedLaunch {
+  const void* q;
+  long long q_stride;  // elements between tokens
+  const void* k_pages;
+  const void* v_pages;
+  const uint8_t* k_scales = nullptr;  // not null: e4m3 pages
+  const uint8_t* v_scales = nullptr;
+  const int32_t* cu_q = nullptr;  // null: one token per sequence
+  const int32_t* table;
+  const int32_t* seqlens;
+  void* o;
+  float* lse;
+  long long lse_head, lse_row;  // strides of lse over heads and tokens
+  int B, Hq, Hkv, total_q, max_q, max_k, d, num_pages, page_size, max_pages, causal;
+  float scale;
+  void* workspace;
+  unsigned long long timeout_ns;
+};
+fa_status launch_paged(const PagedLaunch& a, cudaStream_t stream);
+size_t paged_workspace_bytes();
 
 size_t decode_workspace_bytes(int B, int H, int d, const DecodePlan& plan);
 

@@ -1,0 +1,940 @@
+// paged_sm100.cu -- attention of few new rows per sequence over a paged key/value
+// cache in bf16 or 8 bits (B200, sm_100a).
+//
+// What it computes: sequence b has n_b new query tokens (its last ones) and L_b keys
+// in pages; query head h reads key head h / G, G = Hq / Hkv.  For every new token i
+//     x_ij = scale * q_i . k_j,  j <= L_b - n_b + i (causal) or j < L_b,
+//     o_i  = sum_j softmax_j(x_ij) v_j,   lse_i = ln sum_j exp(x_ij).
+// The G query heads of a key head share its keys, so the n_b G rows (token, head of
+// the group) of one (sequence, key head) are one problem: every key is read once
+// for all of them.  With few rows the cache's bytes are the floor; the tensor cores
+// do the arithmetic because G rows per key are too much of it for the FMA pipes at
+// the rate at which 8 bit keys arrive.
+//
+// B200 design
+//  * Transposed products.  A tile of 128 keys is the M side: S^T [128 keys, N rows] =
+//    K Q^T and O^T [128 dims, N rows] += V^T P^T, with N = 16, 32 or 64 rows, so a
+//    tile of few rows does not pay for 128.  Lane of tensor memory = key (then
+//    dim), column = row: a softmax thread owns one key and N scores.
+//  * 8 bit cache without conversion.  K and V tiles stay e4m3 in shared memory and are
+//    multiplied by kind::f8f6f4 MMAs.  The bf16 row of Q is split into two e4m3
+//    pieces, q = q1 + q2: four significant bits each make bf16's eight, exact but
+//    for elements under 2^-9 of the row's largest, off by at most 2^-17 of it (e4m3's
+//    subnormal step).  The weights are split the same way, p = p1 + p2, off by at most
+//    2^-8 of p, as in bf16, or 2^-17 of the row's largest weight.  Both pieces add into
+//    the same accumulator.
+//    The key scales multiply the scores in fp32; the value scales 2^e_j are carried
+//    in the weights: with y_j = x_j log2(e) + e_j the weight is 2^(y_j - m), m the
+//    running maximum of y, and the sum takes it times 2^-e_j.
+//  * d = 64 runs two key heads side by side as one of 128 dims: the rows of the first
+//    head have zeros in the second's dims and the other way round, and each keeps
+//    its own half of O^T.  Half of the product is wasted; the bytes are the floor.
+//  * Tiles of the cache come by TMA: boxes of gcd(page_size, 128) keys, one page
+//    lookup each, from any page size; a tile's rows past the sequence's end are not
+//    loaded, and its V rows there are zeroed (stale shared memory could hold NaN,
+//    which a weight of zero does not remove).
+//  * The running maximum moves only when some key exceeds it by more than a
+//    threshold: a tile costs one barrier that ORs "does any of my scores exceed",
+//    and the reduction across the 128 keys happens only then.  The l sums stay per
+//    thread until the end.  bf16 keeps two: of the weights as the product takes them
+//    (divides O) and of the unrounded ones (gives lse).  8 bit divides O by the
+//    unrounded sum: its weights carry the value scales, so that a key of quiet values
+//    may round to nothing in the product and still count fully in the sum.
+//  * Work split: (sequence, key head, row tile) units cost ceil(L / 128) tiles; the
+//    line of all units' tiles is cut into equal parts, one per CTA (one CTA per SM),
+//    whatever the lengths.  A unit that lies in one CTA is finished there; others
+//    leave fp32 partial states, two at most per CTA, that paged_merge_kernel joins
+//    in order.  No atomics: results do not depend on timing.
+//  * Warp roles: 0 TMA producer, 1 MMA issuer, 2-5 softmax and epilogue.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "fa_internal.h"
+#include "ptx.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kTile = 128;  // keys per tile
+
+// Exponent offset and threshold of the running maximum, log2 units.  8 bit: weights
+// up to 2^(7 + 1) use e4m3's range (448) and leave the second piece a floor of
+// 2^-10 / 2^7.  bf16: as in the dense forward.
+template <bool kQ8>
+struct SoftmaxRange {
+  static constexpr float kOffset = kQ8 ? 7.f : 0.f;
+  static constexpr float kThreshold = kQ8 ? 1.f : 8.f;
+};
+
+template <int N, bool kQ8>
+struct PagedLayout {
+  static constexpr int kSlotBytes = kTile * 128 * (kQ8 ? 1 : 2);  // one K or V tile
+  static constexpr int kSlots = (kQ8 ? 2 : 1) * (N == 64 ? 5 : 6);
+  static constexpr int kRowBlock = N * 128;      // one 128-byte column block of the N rows
+  static constexpr int kOffQ = kSlots * kSlotBytes;  // two e4m3 pieces, or two 64-dim blocks
+  static constexpr int kOffP = kOffQ + 2 * kRowBlock;  // double buffer of two pieces / 64-key blocks
+  static constexpr int kOffBar = kOffP + 4 * kRowBlock;
+  // kv_full[S], kv_empty[S], q_full, s_full[2], s_free[2], p_full[2], p_free[2]
+  static constexpr int kNumBars = 2 * kSlots + 9;
+  static constexpr int kOffMisc = kOffBar + ((kNumBars * 8 + 15) & ~15);
+  static constexpr int kOffRows = kOffMisc + 64;
+  // per row: factor, limit, threshold, reference, rescale, running max, output row; per warp and row: two sums
+  static constexpr int kSmemBytes = kOffRows + 7 * N * 4 + 8 * N * 4 + 1024;  // + alignment slack
+  static constexpr uint32_t kTmemCols = N == 16 ? 64 : (N == 32 ? 128 : 256);  // S, S, O: 3 N
+};
+
+struct PagedArgs {
+  const __nv_bfloat16* q;
+  long long q_stride;  // elements between tokens
+  __nv_bfloat16* o;
+  float* lse;
+  long long lse_head, lse_row;  // strides of lse
+  const int32_t* cu_q;          // null: one token per sequence
+  const int32_t* table;
+  const int32_t* seqlens;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  int* status;
+  int B, Hq, Hkv, G, groups;  // groups: key heads (d = 128) or pairs of them (d = 64)
+  int total_q, max_q, max_k;
+  int num_pages, page_size, max_pages, box_rows;
+  int causal;
+  float scale_log2;
+  int4* meta;       // [CTAs]: parts of the unit that begins in this CTA and ends in a later one
+  int* part_rows;   // [CTAs, N] its rows' output rows (-1: none)
+  float* part_m;    // [2 CTAs, N] reference, log2 units
+  float* part_l;    // [2 CTAs, N] sum of the unrounded weights
+  float* part_lr;   // [2 CTAs, N] the sum that divides O
+  float* part_o;    // [2 CTAs, N, 128]
+  unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns) {
+  bool ok = true;
+  if (lane_id() == 0) ok = mbar_wait(bar, parity, timeout_ns);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// Sequence b: new tokens, keys and first packed row; nq = -1 when its offsets do not fit.
+struct SeqInfo {
+  int nq, lk, qoff;
+};
+__device__ __forceinline__ SeqInfo seq_info(const PagedArgs& a, int b) {
+  SeqInfo s;
+  s.lk = max(0, min(a.seqlens[b], a.max_k));
+  if (a.cu_q == nullptr) {
+    s.nq = 1;
+    s.qoff = b;
+    return s;
+  }
+  s.qoff = a.cu_q[b];
+  const int end = a.cu_q[b + 1];
+  if (s.qoff < 0 || end < s.qoff || end > a.total_q) {
+    s.nq = -1;
+    return s;
+  }
+  s.nq = min(end - s.qoff, a.max_q);
+  return s;
+}
+
+// rows of one tile that belong to one key head
+template <int N, int D>
+__host__ __device__ constexpr int head_rows() {
+  return D == 64 ? N / 2 : N;
+}
+
+template <int N, int D>
+__device__ __forceinline__ int row_tiles(const PagedArgs& a, int nq) {
+  return nq <= 0 ? 0 : (nq * a.G + head_rows<N, D>() - 1) / head_rows<N, D>();
+}
+
+// Tiles of one unit of a sequence (one, fully masked, when it has no key).
+__device__ __forceinline__ int unit_tiles(int lk) { return max(1, (lk + kTile - 1) / kTile); }
+
+// This CTA's stretch [pos, end) of the line of tiles, as pieces of units.
+struct Work {
+  long long pos, end, total;
+  int b, off;  // sequence of pos, and pos's place among its tiles
+  int ctas;    // CTAs that have a stretch
+};
+struct Piece {
+  int b, hg, rt, t0, t1, tiles;
+  SeqInfo s;
+};
+template <int N, int D>
+__device__ __forceinline__ bool next_piece(const PagedArgs& a, Work& w, Piece& p) {
+  if (w.pos >= w.end) return false;
+  for (; w.b < a.B; ++w.b) {
+    p.s = seq_info(a, w.b);
+    const int rts = row_tiles<N, D>(a, p.s.nq);
+    p.tiles = unit_tiles(p.s.lk);
+    const int cost = rts * a.groups * p.tiles;
+    if (w.off < cost) {
+      const int u = w.off / p.tiles;
+      p.b = w.b;
+      p.hg = u / rts;
+      p.rt = u - p.hg * rts;
+      p.t0 = w.off - u * p.tiles;
+      p.t1 = (int)min((long long)p.tiles, p.t0 + (w.end - w.pos));
+      w.pos += p.t1 - p.t0;
+      w.off += p.t1 - p.t0;
+      return true;
+    }
+    w.off -= cost;
+  }
+  return false;
+}
+
+// Run by one warp: the line's length and where this CTA's stretch begins.
+template <int N, int D>
+__device__ __forceinline__ Work find_work(const PagedArgs& a) {
+  const int lane = lane_id();
+  Work w;
+  auto cost_of = [&](int b) {
+    if (b >= a.B) return 0;
+    const SeqInfo s = seq_info(a, b);
+    return row_tiles<N, D>(a, s.nq) * a.groups * unit_tiles(s.lk);
+  };
+  long long total = 0;
+  for (int b = lane; b < a.B; b += 32) {
+    total += cost_of(b);
+    if (blockIdx.x == 0 && a.cu_q != nullptr && seq_info(a, b).nq < 0) atomicExch(a.status, kStatusBadArg);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  w.total = total;
+  w.ctas = (int)min((long long)gridDim.x, total);
+  w.b = 0;
+  w.off = 0;
+  w.pos = w.end = 0;
+  if ((int)blockIdx.x >= w.ctas) return w;
+  w.pos = total * blockIdx.x / w.ctas;
+  w.end = total * (blockIdx.x + 1) / w.ctas;
+  long long before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int mine = cost_of(b0 + lane);
+    long long upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += x;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + upto > w.pos);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      w.b = b0 + src;
+      w.off = (int)(w.pos - (before + __shfl_sync(0xffffffffu, upto - mine, src)));
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return w;
+}
+
+// Row of the flattened pages that holds key j of sequence b (a page outside the cache is
+// recorded and read as page 0).
+__device__ __forceinline__ int cache_row(const PagedArgs& a, int b, int j) {
+  int page = __ldg(a.table + (size_t)b * a.max_pages + j / a.page_size);
+  if (page < 0 || page >= a.num_pages) {
+    atomicExch(a.status, kStatusBadArg);
+    page = 0;
+  }
+  return page * a.page_size + j % a.page_size;
+}
+
+__device__ __forceinline__ float redux_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+
+// Does `pred` hold in any of the 128 softmax threads?  (Also their barrier.)
+__device__ __forceinline__ bool any_of_group(bool pred) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)pred)
+      : "memory");
+  return any != 0;
+}
+
+// x to the nearest e4m3 pair and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 of_e4m3x2(uint32_t q) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)q, __NV_E4M3)));
+}
+
+// Lane i (mod 32) ends with the sum over the warp of everyone's v[i]; v is used up.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N]) {
+  static_assert(N == 16 || N == 32, "one value per lane at most");
+  const uint32_t lane = lane_id();
+  int live = N;
+  if constexpr (N == 16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+  }
+#pragma unroll
+  for (int off = N / 2; off > 0; off >>= 1) {
+    const bool up = (lane & off) != 0;
+#pragma unroll
+    for (int i = 0; i < off; ++i) {
+      const float give = up ? v[i] : v[i + off];
+      const float keep = up ? v[i + off] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+    }
+    live = off;
+  }
+  (void)live;
+  return v[0];
+}
+
+template <int N, bool kQ8, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
+  using L = PagedLayout<N, kQ8>;
+  using R = SoftmaxRange<kQ8>;
+  constexpr int kHeadRows = head_rows<N, D>();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* kv_full = bars;
+  uint64_t* kv_empty = bars + L::kSlots;
+  uint64_t* q_full = bars + 2 * L::kSlots;
+  uint64_t* s_full = q_full + 1;
+  uint64_t* s_free = q_full + 3;
+  uint64_t* p_full = q_full + 5;
+  uint64_t* p_free = q_full + 7;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+  // a softmax wait gave up: set before the tile's first barrier or after its last, read between
+  volatile int* group_dead = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 8);
+  Work* work = reinterpret_cast<Work*>(smem + L::kOffMisc + 16);
+  static_assert(sizeof(Work) <= 48, "the stretch fits its place");
+  const uint32_t warp = warp_id(), lane = lane_id();
+
+  if (warp == 2) {
+    const Work w = find_work<N, D>(a);
+    if (lane == 0) {
+      *work = w;
+      a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kSlots; ++s) {
+      mbar_init(kv_full + s, 1);
+      mbar_init(kv_empty + s, 1);
+    }
+    mbar_init(q_full, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(s_free + i, 4);
+      mbar_init(p_full + i, 4);
+      mbar_init(p_free + i, 1);
+    }
+    *abort_flag = 0;
+    *group_dead = 0;
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Work w = *work;
+  auto give_up = [&]() {
+    *abort_flag = 1;
+    atomicCAS(a.status, 0, kStatusTimeout);
+  };
+
+  if (warp == 0) {
+    // -------------------------------------------------------------------- TMA producer
+    const int boxes = kTile / a.box_rows;
+    const uint32_t box_bytes = (uint32_t)a.box_rows * 128 * (kQ8 ? 1 : 2);
+    uint32_t g = 0;
+    bool ok = true;
+    Piece p;
+    while (ok && next_piece<N, D>(a, w, p)) {
+      for (int t = p.t0; ok && t < p.t1; ++t) {
+        const int key0 = t * kTile;
+        const int valid = max(0, min(boxes, (p.s.lk - key0 + a.box_rows - 1) / a.box_rows));
+        for (int kv = 0; ok && kv < 2; ++kv, ++g) {
+          const uint32_t slot = g % L::kSlots;
+          if (lane == 0) {
+            ok = mbar_wait(kv_empty + slot, ((g / L::kSlots) & 1) ^ 1, a.timeout_ns) && !*abort_flag;
+            if (!ok)
+              give_up();
+            else if (valid > 0)
+              mbar_arrive_expect_tx(kv_full + slot, valid * box_bytes);
+            else
+              mbar_arrive(kv_full + slot);
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          uint8_t* dst = smem + slot * L::kSlotBytes;
+          const CUtensorMap* map = kv ? &tmV : &tmK;
+          for (int i = lane; i < valid; i += 32) {
+            const int row = cache_row(a, p.b, key0 + i * a.box_rows);
+            uint8_t* to = dst + i * a.box_rows * 128;
+            if constexpr (kQ8) {
+              tma_load_2d(to, map, kv_full + slot, p.hg * 128, row);
+            } else {
+              const int x = p.hg * 128;
+              tma_load_2d(to, map, kv_full + slot, x, row);
+              tma_load_2d(to + kTile * 128, map, kv_full + slot, x + 64, row);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (!ok && lane == 0)  // copies already issued land before the CTA retires
+      for (uint32_t i = g > L::kSlots ? g - L::kSlots : 0; i < g; ++i)
+        (void)mbar_wait(kv_full + (i % L::kSlots), (i / L::kSlots) & 1, a.timeout_ns);
+  } else if (warp == 1) {
+    // -------------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = kQ8 ? idesc_e4m3_f32(128, N, false, false) : idesc_bf16_f32(128, N, false, false);
+      constexpr uint32_t kIdescO = kQ8 ? idesc_e4m3_f32(128, N, true, false) : idesc_bf16_f32(128, N, true, false);
+      const uint32_t base = smem_u32(smem);
+      const SDesc k_desc = sdesc_make(base, 16, 1024);                     // K-major keys
+      const SDesc v_desc = sdesc_make(base, kQ8 ? 16 : 16384, 1024);       // dims along M: MN-major
+      const SDesc q_desc = sdesc_make(base + L::kOffQ, 16, 1024);
+      const SDesc p_desc = sdesc_make(base + L::kOffP, 16, 1024);
+      constexpr uint32_t kSlot16 = L::kSlotBytes / 16, kBlock16 = L::kRowBlock / 16;
+      const uint32_t tO = tmem + 2 * N;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && (!mbar_wait(bar, parity, a.timeout_ns) || *abort_flag)) {
+          give_up();
+          ok = false;
+        }
+        return ok;
+      };
+      auto product = [&](uint32_t d, SDesc x, uint32_t x_step, SDesc y, uint32_t idesc, bool accumulate) {
+        // 8 bit: 4 steps of 32, for each of y's two pieces; bf16: 8 steps of 16 over two blocks
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t xo = kQ8 ? (i & 3) * x_step : (x_step == 2 ? (i >> 2) * 1024 + (i & 3) * 2 : i * x_step);
+          const uint64_t xd = sdesc_at(x, xo), yd = sdesc_at(y, (i >> 2) * kBlock16 + (i & 3) * 2);
+          if constexpr (kQ8)
+            umma_ss_f8(d, xd, yd, idesc, (accumulate || i > 0) ? 1u : 0u);
+          else
+            umma_ss(d, xd, yd, idesc, (accumulate || i > 0) ? 1u : 0u);
+        }
+      };
+      uint32_t c = 0, piece = 0;  // tiles and pieces so far
+      auto pv = [&](uint32_t x, bool accumulate) {
+        const uint32_t slot = (2 * x + 1) % L::kSlots;
+        if (!wait(p_full + (x & 1), (x >> 1) & 1)) return;
+        if (!wait(kv_full + slot, ((2 * x + 1) / L::kSlots) & 1)) return;
+        tc_fence_after();
+        product(tO, SDesc{v_desc.lo + slot * kSlot16, v_desc.hi}, kQ8 ? 256 : 128,
+                SDesc{p_desc.lo + (x & 1) * 2 * kBlock16, p_desc.hi}, kIdescO, accumulate);
+        umma_commit(p_free + (x & 1));
+        umma_commit(kv_empty + slot);
+      };
+      Piece p;
+      while (ok && next_piece<N, D>(a, w, p)) {
+        if (!wait(q_full, piece++ & 1)) break;
+        tc_fence_after();
+        const int n = p.t1 - p.t0;
+        for (int t = 0; ok && t < n; ++t, ++c) {
+          const uint32_t slot = (2 * c) % L::kSlots;
+          if (!wait(kv_full + slot, ((2 * c) / L::kSlots) & 1)) break;
+          if (c >= 2 && !wait(s_free + (c & 1), ((c >> 1) - 1) & 1)) break;
+          tc_fence_after();
+          product(tmem + (c & 1) * N, SDesc{k_desc.lo + slot * kSlot16, k_desc.hi}, 2, q_desc, kIdescS, false);
+          umma_commit(s_full + (c & 1));
+          umma_commit(kv_empty + slot);
+          if (t > 0) pv(c - 1, t > 1);
+        }
+        if (ok) pv(c - 1, n > 1);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------------- softmax and epilogue
+    const uint32_t quarter = warp & 3;
+    const int r = quarter * 32 + lane;         // key of the tile, then dim of O
+    const int tid = threadIdx.x - 64;          // 0 .. 127
+    const uint32_t lanes = (quarter * 32) << 16;
+    float* factor = reinterpret_cast<float*>(smem + L::kOffRows);  // of the scores: scale, log2 e, Q's scale
+    int* limit = reinterpret_cast<int*>(factor + N);               // first key that the row does not see
+    float* thresh = factor + 2 * N;  // running maximum + threshold
+    float* ref = factor + 3 * N;     // what the weights' exponents are taken from
+    float* alpha = factor + 4 * N;
+    float* top = factor + 5 * N;     // running maximum
+    int* out_row = reinterpret_cast<int*>(factor + 6 * N);  // token * Hq + head, -1: no row
+    float* wred = factor + 7 * N;    // [4][N] maxima, then sums
+    float* wred2 = wred + 4 * N;
+    uint32_t c = 0;
+    // A wait that gives up does not leave at once: the group's barriers need all four
+    // warps, so the warp goes on (waiting no more) to the next place where all leave
+    // together.
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok && (!warp_wait(bar, parity, a.timeout_ns) || *abort_flag)) {
+        if (lane == 0) {
+          give_up();
+          *group_dead = 1;
+        }
+        __syncwarp();
+        ok = false;
+      }
+    };
+    Piece p;
+    while (next_piece<N, D>(a, w, p)) {
+      const int tiles = p.t1 - p.t0;
+      // ---- the piece's rows: kThreadsPerRow threads share a row of 128 dims
+      {
+        constexpr int kTpr = 128 / N, kPer = 128 / kTpr;  // threads per row, dims per thread
+        const int n = tid / kTpr, d0 = (tid % kTpr) * kPer;
+        const int half = D == 64 ? n / kHeadRows : 0;   // which of the pair's heads
+        const int row = p.rt * kHeadRows + (D == 64 ? n % kHeadRows : n);
+        const int token = row / a.G, hk = D == 64 ? 2 * p.hg + half : p.hg;
+        const bool have = token < p.s.nq && hk < a.Hkv;
+        const int head = hk * a.G + row % a.G;
+        // dims d0 .. d0 + kPer - 1 of the 128: this row's head has its own D of them
+        const bool mine = have && (D == 128 || d0 / 64 == half);
+        const __nv_bfloat16* src = a.q + (long long)(p.s.qoff + token) * a.q_stride + (long long)head * D + (D == 64 ? d0 % 64 : d0);
+        uint32_t qw[kPer / 2];
+#pragma unroll
+        for (int i = 0; i < kPer / 8; ++i) {
+          const uint4 x = mine ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+          qw[4 * i] = x.x, qw[4 * i + 1] = x.y, qw[4 * i + 2] = x.z, qw[4 * i + 3] = x.w;
+        }
+        float f = a.scale_log2;
+        const uint32_t row_at = smem_u32(smem + L::kOffQ) + n * 128;
+        if constexpr (kQ8) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < kPer / 2; ++i) m = __vmaxu2(m, qw[i] & 0x7FFF7FFFu);
+          m = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+          for (int off = 1; off < kTpr; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+          // times 2^(7 - exponent): the largest element in [128, 256)
+          const int e = m == 0 ? 0 : min(120, max(-112, (int)(m >> 7) - 127 - 7));
+          const float up = __uint_as_float((uint32_t)(127 - e) << 23);
+          f *= __uint_as_float((uint32_t)(127 + e) << 23);
+          if (m >= 0x7F80u) f = __uint_as_float(0x7FC00000u);  // an infinity or NaN in the row: NaN scores
+#pragma unroll
+          for (int i = 0; i < kPer / 16; ++i) {
+            uint32_t q1[4], q2[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t h1[2], h2[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t x = qw[8 * i + 2 * j + k];
+                const float lo = __uint_as_float(x << 16) * up, hi = __uint_as_float(x & 0xFFFF0000u) * up;
+                h1[k] = to_e4m3x2(lo, hi);
+                const float2 back = of_e4m3x2(h1[k]);
+                h2[k] = to_e4m3x2(lo - back.x, hi - back.y);
+              }
+              q1[j] = h1[0] | (h1[1] << 16);
+              q2[j] = h2[0] | (h2[1] << 16);
+            }
+            const uint32_t at = row_at + ((((d0 >> 4) + i) ^ (n & 7)) << 4);
+            st_shared_v4(at, q1[0], q1[1], q1[2], q1[3]);
+            st_shared_v4(at + L::kRowBlock, q2[0], q2[1], q2[2], q2[3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPer / 8; ++i) {
+            const int chunk = (d0 >> 3) + i;  // of 16: two blocks of 64 dims
+            st_shared_v4(row_at + (chunk >> 3) * L::kRowBlock + (((chunk & 7) ^ (n & 7)) << 4), qw[4 * i], qw[4 * i + 1],
+                         qw[4 * i + 2], qw[4 * i + 3]);
+          }
+        }
+        if (tid % kTpr == 0) {
+          factor[n] = have ? f : 0.f;
+          limit[n] = (have && a.causal) ? max(0, min(p.s.lk, p.s.lk - p.s.nq + token + 1)) : p.s.lk;
+          thresh[n] = -INFINITY;
+          top[n] = -INFINITY;
+          ref[n] = -R::kOffset;
+          out_row[n] = have ? (p.s.qoff + token) * a.Hq + head : -1;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive_warp(q_full);
+      named_bar_sync(1, 128);
+      // keys that every row of the tile sees: [0, all_see)
+      const int first_token = (p.rt * kHeadRows) / a.G;
+      const int all_see = a.causal ? max(0, min(p.s.lk, p.s.lk - p.s.nq + first_token + 1)) : p.s.lk;
+
+      float l[N], lr[kQ8 ? 1 : N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        l[n] = 0.f;
+        if constexpr (!kQ8) lr[n] = 0.f;
+      }
+
+      for (int t = 0; t < tiles; ++t, ++c) {
+        const int key = (p.t0 + t) * kTile + r;
+        const int tile_end = (p.t0 + t + 1) * kTile;
+        // the key's scales (two heads' when d = 64), while its scores are made
+        float kf[2] = {1.f, 1.f}, ve[2] = {0.f, 0.f}, vinv[2] = {1.f, 1.f};
+        if constexpr (kQ8) {
+          if (key < p.s.lk) {
+            const size_t at = (size_t)cache_row(a, p.b, key) * a.Hkv;
+#pragma unroll
+            for (int h = 0; h < (D == 64 ? 2 : 1); ++h) {
+              const int hk = D == 64 ? 2 * p.hg + h : p.hg;
+              if (hk < a.Hkv) {
+                kf[h] = __uint_as_float((uint32_t)__ldg(a.k_scales + at + hk) << 23);
+                const int e = (int)__ldg(a.v_scales + at + hk) - 127;
+                ve[h] = (float)e;
+                vinv[h] = __uint_as_float((uint32_t)(127 - e) << 23);
+              }
+            }
+          }
+        }
+        wait(s_full + (c & 1), (c >> 1) & 1);
+        tc_fence_after();
+        float y[N];
+        tmem_ld_cols<N>(tmem + lanes + (c & 1) * N, y);
+        tc_fence_before();
+        mbar_arrive_warp(s_free + (c & 1));
+        const bool masked = tile_end > all_see;
+        bool over = !ok;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const int h = (D == 64 && n >= kHeadRows) ? 1 : 0;
+          float x = y[n] * factor[n];
+          if constexpr (kQ8) x = fmaf(x, kf[h], ve[h]);
+          if (masked && key >= limit[n]) x = -INFINITY;
+          y[n] = x;
+          over |= x > thresh[n];
+        }
+        if (any_of_group(over)) {
+          // some key exceeds its row's running maximum: the tile's maximum of every row
+#pragma unroll
+          for (int n0 = 0; n0 < N; n0 += 32) {
+            float mine = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < (N < 32 ? N : 32); ++i) {
+              const float m = redux_max(y[n0 + i]);
+              if (lane == (uint32_t)i) mine = m;
+            }
+            if (n0 + (int)lane < N) wred[quarter * N + n0 + lane] = mine;
+          }
+          const bool dead = *group_dead != 0;
+          named_bar_sync(1, 128);
+          if (dead) {
+            ok = false;
+            break;
+          }
+          if (tid < N) {
+            const float m = fmaxf(fmaxf(wred[tid], wred[N + tid]), fmaxf(wred[2 * N + tid], wred[3 * N + tid]));
+            const float old = top[tid];
+            float al = 1.f;
+            if (m > thresh[tid]) {
+              al = old == -INFINITY ? 0.f : ex2(old - m);
+              top[tid] = m;
+              thresh[tid] = m + R::kThreshold;
+              ref[tid] = m - R::kOffset;
+            }
+            alpha[tid] = al;
+          }
+          named_bar_sync(1, 128);
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            l[n] *= alpha[n];
+            if constexpr (!kQ8) lr[n] *= alpha[n];
+          }
+          if (t > 0) {  // O holds earlier tiles: rescale it once the last product is in
+            wait(p_free + ((c - 1) & 1), ((c - 1) >> 1) & 1);
+            tc_fence_after();
+            uint32_t o[16];
+#pragma unroll 1
+            for (int n0 = 0; n0 < N; n0 += 16) {
+              tmem_ld16(tmem + lanes + 2 * N + n0, o);
+              tmem_ld_wait16(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[n0 + i]);
+              tmem_st16(tmem + lanes + 2 * N + n0, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        // weights; the buffer is free once the product of two tiles ago has read it
+        if (c >= 2) wait(p_free + (c & 1), ((c >> 1) - 1) & 1);
+        const uint32_t pbuf = smem_u32(smem + L::kOffP) + (c & 1) * 2 * L::kRowBlock;
+#pragma unroll
+        for (int n = 0; n < N; n += 2) {
+          const int h = (D == 64 && n >= kHeadRows) ? 1 : 0;
+          const float2 pw = make_float2(ex2(y[n] - ref[n]), ex2(y[n + 1] - ref[n + 1]));
+          l[n] = fmaf(pw.x, vinv[h], l[n]);
+          l[n + 1] = fmaf(pw.y, vinv[h], l[n + 1]);
+          if constexpr (kQ8) {
+            const uint32_t p1 = to_e4m3x2(pw.x, pw.y);
+            const float2 b1 = of_e4m3x2(p1);
+            const uint32_t p2 = to_e4m3x2(pw.x - b1.x, pw.y - b1.y);
+            const uint32_t at0 = pbuf + n * 128 + (((r >> 4) ^ (n & 7)) << 4) + (r & 15);
+            const uint32_t at1 = pbuf + (n + 1) * 128 + (((r >> 4) ^ ((n + 1) & 7)) << 4) + (r & 15);
+            st_shared_u8(at0, p1);
+            st_shared_u8(at1, p1 >> 8);
+            st_shared_u8(at0 + L::kRowBlock, p2);
+            st_shared_u8(at1 + L::kRowBlock, p2 >> 8);
+          } else {
+            const uint32_t k2 = pack_bf16x2(pw.x, pw.y);
+            lr[n] += __uint_as_float(k2 << 16);
+            lr[n + 1] += __uint_as_float(k2 & 0xFFFF0000u);
+            const uint32_t block = pbuf + (r >> 6) * L::kRowBlock, chunk = (r & 63) >> 3, in = (r & 7) * 2;
+            st_shared_u16(block + n * 128 + ((chunk ^ (n & 7)) << 4) + in, k2);
+            st_shared_u16(block + (n + 1) * 128 + ((chunk ^ ((n + 1) & 7)) << 4) + in, k2 >> 16);
+          }
+        }
+        if (tile_end > p.s.lk) {
+          // V rows past the sequence's end: whatever the slot or the page holds there
+          // becomes zero
+          const uint32_t slot = (2 * c + 1) % L::kSlots;
+          wait(kv_full + slot, ((2 * c + 1) / L::kSlots) & 1);
+          if (key >= p.s.lk) {
+            const uint32_t at = smem_u32(smem + slot * L::kSlotBytes) + r * 128;
+#pragma unroll
+            for (int i = 0; i < (kQ8 ? 8 : 16); ++i) st_shared_v4(at + (i >> 3) * kTile * 128 + (i & 7) * 16, 0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive_warp(p_full + (c & 1));
+      }
+      // ---- epilogue: all products of the piece are in (a group that broke off has ok =
+      // false in every warp and leaves here)
+      if (ok) wait(p_free + ((c - 1) & 1), ((c - 1) >> 1) & 1);
+      if (any_of_group(!ok)) break;
+      tc_fence_after();
+      constexpr int kSum = N < 32 ? N : 32;
+#pragma unroll
+      for (int n0 = 0; n0 < N; n0 += 32) {
+        float v1[kSum], v2[kSum];
+#pragma unroll
+        for (int i = 0; i < kSum; ++i) {
+          v1[i] = l[n0 + i];
+          if constexpr (!kQ8) v2[i] = lr[n0 + i];
+        }
+        const float s1 = warp_sums<kSum>(v1);
+        float s2 = s1;
+        if constexpr (!kQ8) s2 = warp_sums<kSum>(v2);
+        if ((int)lane < kSum) {
+          wred[quarter * N + n0 + lane] = s1;
+          wred2[quarter * N + n0 + lane] = s2;
+        }
+      }
+      named_bar_sync(1, 128);
+      float o[N];
+      tmem_ld_cols<N>(tmem + lanes + 2 * N, o);
+      const bool whole = p.t0 == 0 && p.t1 == p.tiles;
+      if (whole) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const float sum = (wred2[n] + wred2[N + n]) + (wred2[2 * N + n] + wred2[3 * N + n]);
+          const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+          const int row = out_row[n];
+          const bool mine = D == 128 || (n >= kHeadRows) == (r >= 64);
+          if (row >= 0 && mine) a.o[(size_t)row * D + (D == 64 ? (r & 63) : r)] = __float2bfloat16(o[n] * inv);
+        }
+        if (tid < N && out_row[tid] >= 0) {
+          const float sum = (wred[tid] + wred[N + tid]) + (wred[2 * N + tid] + wred[3 * N + tid]);
+          const int token = out_row[tid] / a.Hq, head = out_row[tid] - token * a.Hq;
+          a.lse[token * a.lse_row + head * a.lse_head] =
+              sum == 0.f ? -INFINITY : (ref[tid] + __log2f(sum)) * 0.69314718055994530942f;
+        }
+      } else {
+        // slot 0: a piece that goes on with a unit begun before; slot 1: a unit begun here
+        const size_t slot = 2 * (size_t)blockIdx.x + (p.t0 == 0 ? 1 : 0);
+#pragma unroll
+        for (int n = 0; n < N; ++n) a.part_o[(slot * N + n) * 128 + r] = o[n];
+        if (tid < N) {
+          a.part_m[slot * N + tid] = ref[tid];
+          a.part_l[slot * N + tid] = (wred[tid] + wred[N + tid]) + (wred[2 * N + tid] + wred[3 * N + tid]);
+          a.part_lr[slot * N + tid] = (wred2[tid] + wred2[N + tid]) + (wred2[2 * N + tid] + wred2[3 * N + tid]);
+          if (p.t0 == 0) a.part_rows[(size_t)blockIdx.x * N + tid] = out_row[tid];
+        }
+        if (p.t0 == 0 && tid == 0) {
+          // the CTA that has the unit's last tile
+          const long long last = w.pos - p.t1 + p.tiles - 1;
+          a.meta[blockIdx.x] = make_int4((int)(((last + 1) * w.ctas - 1) / w.total) - (int)blockIdx.x + 1, 0, 0, 0);
+        }
+      }
+      named_bar_sync(1, 128);  // the rows' places are written again for the next piece
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+// Joins the partial states of the unit that begins in attention CTA blockIdx.x (none:
+// nothing to do), a warp per row: with M the largest reference, every part's sums and
+// O count 2^(m - M).  Part 0 is that CTA's slot 1, part i the slot 0 of CTA + i.
+template <int N, int D>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
+  const int cta = blockIdx.x, parts = a.meta[cta].x;
+  if (parts == 0) return;
+  const int n = blockIdx.y * 4 + warp_id(), lane = lane_id();
+  const int row = a.part_rows[(size_t)cta * N + n];
+  if (row < 0) return;
+  auto at = [&](int i) { return (2 * (size_t)(cta + i) + (i == 0 ? 1 : 0)) * N + n; };
+  float M = -INFINITY;
+  for (int i = lane; i < parts; i += 32)
+    if (a.part_l[at(i)] != 0.f) M = fmaxf(M, a.part_m[at(i)]);
+  M = redux_max(M);
+  constexpr int kPer = D / 32;
+  const int d0 = lane * kPer + (D == 64 && n >= N / 2 ? 64 : 0);
+  float acc[kPer], l = 0.f, lr = 0.f;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < parts; ++i) {
+    const float pl = a.part_l[at(i)];
+    const float wt = pl == 0.f ? 0.f : ex2(a.part_m[at(i)] - M);
+    l = fmaf(wt, pl, l);
+    lr = fmaf(wt, a.part_lr[at(i)], lr);
+    const float* src = a.part_o + at(i) * 128 + d0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, src[e], acc[e]);
+  }
+  const float inv = lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr);
+  __nv_bfloat16* out = a.o + (size_t)row * D + lane * kPer;
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2)
+    *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0) {
+    const int token = row / a.Hq, head = row - token * a.Hq;
+    a.lse[token * a.lse_row + head * a.lse_head] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.69314718055994530942f;
+  }
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct PagedCarve {
+  size_t meta, rows, m, l, lr, o, bytes;
+};
+PagedCarve paged_carve(int ctas, int n) {
+  PagedCarve c;
+  size_t at = kStatusBytes;
+  auto take = [&](size_t b) {
+    const size_t x = at;
+    at += up256(b);
+    return x;
+  };
+  c.meta = take(sizeof(int4) * ctas);
+  c.rows = take(sizeof(int) * ctas * n);
+  c.m = take(sizeof(float) * 2 * ctas * n);
+  c.l = take(sizeof(float) * 2 * ctas * n);
+  c.lr = take(sizeof(float) * 2 * ctas * n);
+  c.o = take(sizeof(float) * 2 * ctas * n * 128);
+  c.bytes = at;
+  return c;
+}
+
+// Rows per tile: the smallest that holds all rows of one key head's longest chunk (two
+// heads' when d = 64), at most 64.
+int paged_rows(const PagedLaunch& L) {
+  const long long rows = (long long)L.max_q * (L.Hq / L.Hkv) * (L.d == 64 ? 2 : 1);
+  return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+}
+
+template <int N, bool kQ8, int D>
+fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
+  using L = PagedLayout<N, kQ8>;
+  static PerDeviceOnce attr_once;
+  if (!attr_once.run([] {
+        return cudaFuncSetAttribute(paged_kernel<N, kQ8, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    L::kSmemBytes) == cudaSuccess;
+      }))
+    return FA_ERR_CUDA;
+  PagedArgs a;
+  int box = 128;
+  while (L0.page_size % box) box /= 2;
+  CUtensorMap tk, tv;
+  const long long rows = (long long)L0.num_pages * L0.page_size;
+  if (!encode_matrix_map(&tk, L0.k_pages, rows, L0.Hkv * D, kQ8, box) ||
+      !encode_matrix_map(&tv, L0.v_pages, rows, L0.Hkv * D, kQ8, box))
+    return FA_ERR_CUDA;
+  const int ctas = num_sms();
+  const PagedCarve c = paged_carve(ctas, N);
+  uint8_t* ws = static_cast<uint8_t*>(L0.workspace);
+  a.q = static_cast<const __nv_bfloat16*>(L0.q);
+  a.q_stride = L0.q_stride;
+  a.o = static_cast<__nv_bfloat16*>(L0.o);
+  a.lse = L0.lse;
+  a.lse_head = L0.lse_head;
+  a.lse_row = L0.lse_row;
+  a.cu_q = L0.cu_q;
+  a.table = L0.table;
+  a.seqlens = L0.seqlens;
+  a.k_scales = L0.k_scales;
+  a.v_scales = L0.v_scales;
+  a.status = reinterpret_cast<int*>(ws);
+  a.B = L0.B;
+  a.Hq = L0.Hq;
+  a.Hkv = L0.Hkv;
+  a.G = L0.Hq / L0.Hkv;
+  a.groups = D == 64 ? (L0.Hkv + 1) / 2 : L0.Hkv;
+  a.total_q = L0.total_q;
+  a.max_q = L0.max_q;
+  a.max_k = L0.max_k;
+  a.num_pages = L0.num_pages;
+  a.page_size = L0.page_size;
+  a.max_pages = L0.max_pages;
+  a.box_rows = box;
+  a.causal = L0.causal;
+  a.scale_log2 = L0.scale * 1.4426950408889634f;
+  a.meta = reinterpret_cast<int4*>(ws + c.meta);
+  a.part_rows = reinterpret_cast<int*>(ws + c.rows);
+  a.part_m = reinterpret_cast<float*>(ws + c.m);
+  a.part_l = reinterpret_cast<float*>(ws + c.l);
+  a.part_lr = reinterpret_cast<float*>(ws + c.lr);
+  a.part_o = reinterpret_cast<float*>(ws + c.o);
+  a.timeout_ns = L0.timeout_ns;
+  prof_before(stream, kKPaged);
+  paged_kernel<N, kQ8, D><<<ctas, kThreads, L::kSmemBytes, stream>>>(tk, tv, a);
+  cudaError_t err = cudaGetLastError();
+  prof_after(stream, kKPaged);
+  if (err != cudaSuccess) return FA_ERR_CUDA;
+  prof_before(stream, kKPagedMerge);
+  paged_merge_kernel<N, D><<<dim3(ctas, N / 4), 128, 0, stream>>>(a);
+  err = cudaGetLastError();
+  prof_after(stream, kKPagedMerge);
+  return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int N>
+fa_status launch_paged_rows(const PagedLaunch& L, cudaStream_t stream) {
+  if (L.k_scales != nullptr)
+    return L.d == 64 ? launch_paged_impl<N, true, 64>(L, stream) : launch_paged_impl<N, true, 128>(L, stream);
+  return L.d == 64 ? launch_paged_impl<N, false, 64>(L, stream) : launch_paged_impl<N, false, 128>(L, stream);
+}
+
+}  // namespace
+
+size_t paged_workspace_bytes() { return paged_carve(num_sms(), 64).bytes; }
+
+fa_status launch_paged(const PagedLaunch& L, cudaStream_t stream) {
+  switch (paged_rows(L)) {
+    case 16: return launch_paged_rows<16>(L, stream);
+    case 32: return launch_paged_rows<32>(L, stream);
+    default: return launch_paged_rows<64>(L, stream);
+  }
+}
+
+}  // namespace fa

@@ -321,6 +321,113 @@ FA_API fa_status fa_decode_paged(const void* q, const void* k_pages, const void*
                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * The paged key/value cache: writing it, reading it back, and attention over it.
+ * (The pages name paging as the batched-decode layout question, "FlashAttention saves
+ * IO, not N^2 work", section 6, and give no format.)
+ *
+ *   k_pages, v_pages : [num_pages, page_size, H, d], any page_size >= 1; key t of
+ *                      sequence b is row t % page_size of page block_table[b][t / page_size]
+ *   k_scales, v_scales : NULL: the pages are bf16.  Not NULL (both): the pages are in 8
+ *                      bits, e4m3 codes with one scale byte per row and head,
+ *                      [num_pages, page_size, H]; a code c of a row with scale byte s
+ *                      stands for c * 2^(s - 127).  fa_cache_write gives s - 127 the
+ *                      smallest whole number e in [-60, 60] with a <= 448 * 2^e, a the
+ *                      largest magnitude among the row's finite values, and rounds
+ *                      x * 2^-e to the nearest e4m3 value (ties to even; magnitudes over
+ *                      448 to 448; infinities and NaN to NaN).  Every stored value is a
+ *                      bf16 number exactly.  Scale bytes outside [67, 187] are not checked
+ *                      and may overflow fp32 inside the attention calls.
+ *   block_table      : device int32 [B, max_pages_per_seq]; entries past a sequence's
+ *                      last page are not read
+ * d in {64, 128}; num_pages * page_size and max_pages_per_seq * page_size < 2^31.
+ * The k, v and q arguments of fa_cache_write and fa_fwd_paged are rows [total, H, d]
+ * with *_row_stride elements between rows (>= H * d, a multiple of 8), so a slice of a
+ * fused projection needs no copy.
+ */
+
+/*
+ * Writes new rows into the pages of their sequences.
+ *   k, v        : [total, H, d] bf16; sequence b owns rows cu_seqlens[b] .. cu_seqlens[b+1]-1
+ *   cu_seqlens  : device int32 [B+1], non-decreasing, 0 <= cu_seqlens[b] <= total
+ *   seqlens_k   : device int32 [B], keys of each sequence after the write: its n_b new rows
+ *                 go to positions seqlens_k[b] - n_b .. seqlens_k[b] - 1
+ *   workspace   : at least 256 bytes (the status word)
+ * Rows of k and v that belong to no sequence are not written anywhere, and no other
+ * row of the pages is touched.  A sequence whose offsets do not fit, with more new rows
+ * than keys, or with a position beyond its block table is skipped, and a row whose page
+ * index lies outside [0, num_pages) is dropped; both are recorded in the status word
+ * (fa_check then returns FA_ERR_INVALID_ARG).  Two rows that share a slot of the pages
+ * leave either's values.
+ */
+FA_API fa_status fa_cache_write(const void* k, const void* v, long long k_row_stride, long long v_row_stride,
+                                const int32_t* cu_seqlens, const int32_t* block_table, const int32_t* seqlens_k,
+                                void* k_pages, void* v_pages, uint8_t* k_scales, uint8_t* v_scales, int B, int H,
+                                int total, int num_pages, int page_size, int max_pages_per_seq, int d,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Reads sequences back into packed bf16 rows (exactly), as fa_fwd_varlen and the packed
+ * decode take them: keys 0 .. n_b - 1 of sequence b, n_b = cu_seqlens_k[b+1] -
+ * cu_seqlens_k[b], go to rows cu_seqlens_k[b] .. of k, v [total_k, H, d].  Other rows
+ * are left as they were.  Bad offsets and page indices as in fa_cache_write: those rows
+ * are not written, and recorded.
+ */
+FA_API fa_status fa_cache_read(const void* k_pages, const void* v_pages, const uint8_t* k_scales,
+                               const uint8_t* v_scales, const int32_t* cu_seqlens_k, const int32_t* block_table,
+                               void* k, void* v, int B, int H, int total_k, int num_pages, int page_size,
+                               int max_pages_per_seq, int d, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/*
+ * Attention of a chunk of new tokens per sequence over a paged cache that already
+ * holds their keys and values (fa_cache_write first).
+ *   q            : [total_q, Hq, d] bf16; sequence b's n_b new tokens are rows
+ *                  cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 and the last n_b of its
+ *                  seqlens_k[b] keys.  Hq is a multiple of Hkv; query head h reads key
+ *                  head h / (Hq / Hkv).
+ *   causal       : bottom-right aligned per sequence: token i sees keys
+ *                  0 .. seqlens_k[b] - n_b + i; else all seqlens_k[b] keys
+ *   seqlens_k    : device int32 [B], clamped to [0, max_seqlen_k]
+ *   max_seqlen_q, max_seqlen_k : upper bounds of n_b and of the lengths (longer chunks
+ *                  are cut to it); max_seqlen_k must not exceed
+ *                  max_pages_per_seq * page_size (FA_ERR_INVALID_ARG)
+ *   o            : [total_q, Hq, d] bf16 (written), contiguous
+ *   lse          : [Hq, total_q] fp32 (written)
+ *   workspace    : at least fa_paged_workspace_size(...) bytes
+ * n_b may be 1 for some or all sequences, and 0.  Tokens that see no key get O = 0 and
+ * LSE = -inf.  Rows behind the last sequence are left as they were.  Page indices
+ * outside the cache are recorded and read as page 0, as in fa_decode_paged; sequences
+ * whose offsets do not fit are skipped and recorded.  A key that some token of the chunk
+ * sees must be finite in the value cache for every token of the sequence (a weight of
+ * zero does not remove an infinity or NaN); rows past a sequence's end may hold anything.
+ * Results do not depend on timing: two calls with the same arguments agree bit for bit.
+ */
+FA_API fa_status fa_fwd_paged(const void* q, long long q_row_stride, const void* k_pages, const void* v_pages,
+                              const uint8_t* k_scales, const uint8_t* v_scales, const int32_t* cu_seqlens_q,
+                              const int32_t* block_table, const int32_t* seqlens_k, void* o, float* lse, int B, int Hq,
+                              int Hkv, int total_q, int num_pages, int page_size, int max_pages_per_seq,
+                              int max_seqlen_q, int max_seqlen_k, int d, int causal, float softmax_scale,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Single-token attention over an 8 bit paged cache: fa_decode_paged for it, with grouped
+ * heads.  q [B, Hq, d] bf16, o [B, Hq, d] bf16, lse [B, Hq] fp32; the other arguments as
+ * for fa_fwd_paged.
+ */
+FA_API fa_status fa_decode_paged_q8(const void* q, const void* k_pages, const void* v_pages, const uint8_t* k_scales,
+                                    const uint8_t* v_scales, const int32_t* block_table, const int32_t* seqlens_k,
+                                    int B, int Hq, int Hkv, int num_pages, int page_size, int max_pages_per_seq,
+                                    int max_seqlen_k, int d, float softmax_scale, void* o, float* lse,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Workspace of fa_fwd_paged and fa_decode_paged_q8 (max_seqlen_q = 1) in bytes, 0 when
+ * the arguments are invalid.  Only its first 256 bytes need to be zero before the first
+ * use.
+ */
+FA_API size_t fa_paged_workspace_size(int B, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int d);
+
+/*
  * fa_decode_splitkv without a workspace, for callers that cannot allocate
  * device memory -- for example an operator inside a host framework that owns
  * every device allocation and offers it no allocator, or a serving loop that
