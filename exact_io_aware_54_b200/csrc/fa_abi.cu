@@ -716,6 +716,8 @@ static fa_status fwd_paged(const void* q, long long q_row_stride, const void* k_
   // every key a sequence may hold must have a block-table entry
   if ((long long)max_seqlen_k > (long long)max_pages * page_size) return FA_ERR_INVALID_ARG;
   if (q_row_stride < (long long)Hq * d) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k_scales) & 3u) || (reinterpret_cast<uintptr_t>(v_scales) & 3u))
+    return FA_ERR_ALIGNMENT;  // scale bytes are loaded by the word
   if (!aligned16(q) || q_row_stride % 8 || !aligned16(o) || !aligned16(lse) ||
       (reinterpret_cast<uintptr_t>(cu_seqlens_q) & 3u) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u))
     return FA_ERR_ALIGNMENT;

@@ -21,18 +21,21 @@
 //    pieces, q = q1 + q2: four significant bits each make bf16's eight, exact but
 //    for elements under 2^-9 of the row's largest, off by at most 2^-17 of it (e4m3's
 //    subnormal step).  The weights are split the same way, p = p1 + p2, off by at most
-//    2^-8 of p, as in bf16, or 2^-17 of the row's largest weight.  Both pieces add into
-//    the same accumulator.
+//    2^-8 of p, as in bf16, or 2^-17 of the row's largest weight.  The two pieces of a row
+//    are two columns of the product, added up when they are read: an MMA costs the same
+//    for 32 or 64 columns as for 16, so a second pass over the tile would cost twice.
 //    The key scales multiply the scores in fp32; the value scales 2^e_j are carried
 //    in the weights: with y_j = x_j log2(e) + e_j the weight is 2^(y_j - m), m the
 //    running maximum of y, and the sum takes it times 2^-e_j.
 //  * d = 64 runs two key heads side by side as one of 128 dims: the rows of the first
 //    head have zeros in the second's dims and the other way round, and each keeps
 //    its own half of O^T.  Half of the product is wasted; the bytes are the floor.
-//  * Tiles of the cache come by TMA: boxes of gcd(page_size, 128) keys, one page
-//    lookup each, from any page size; a tile's rows past the sequence's end are not
-//    loaded, and its V rows there are zeroed (stale shared memory could hold NaN,
-//    which a weight of zero does not remove).
+//  * Tiles of the cache come by 16-byte asynchronous copies, a warp for K and one for V,
+//    each row from wherever its page is, so any page size costs the same; rows past the
+//    sequence's end are filled with zeros (stale shared memory could hold NaN, which a
+//    weight of zero does not remove).  TMA boxes cost some 200 cycles each whatever their
+//    size: with pages of 16 keys 16 of them a tile, 3000 cycles where its bytes take 1400
+//    (64 requests, 8 key heads: 516 us).
 //  * The running maximum moves only when some key exceeds it by more than a
 //    threshold: a tile costs one barrier that ORs "does any of my scores exceed",
 //    and the reduction across the 128 keys happens only then.  The l sums stay per
@@ -40,12 +43,25 @@
 //    (divides O) and of the unrounded ones (gives lse).  8 bit divides O by the
 //    unrounded sum: its weights carry the value scales, so that a key of quiet values
 //    may round to nothing in the product and still count fully in the sum.
-//  * Work split: (sequence, key head, row tile) units cost ceil(L / 128) tiles; the
-//    line of all units' tiles is cut into equal parts, one per CTA (one CTA per SM),
-//    whatever the lengths.  A unit that lies in one CTA is finished there; others
-//    leave fp32 partial states, two at most per CTA, that paged_merge_kernel joins
-//    in order.  No atomics: results do not depend on timing.
-//  * Warp roles: 0 TMA producer, 1 MMA issuer, 2-5 softmax and epilogue.
+//  * Work split: CTAs come in teams of neighbouring key heads, which read the same keys'
+//    neighbouring bytes at about the same time (a head's slice of a row is 128 bytes in 8
+//    bits: alone, such reads leave most of HBM's rate unused, 64 requests of 8 key heads
+//    675 us).  A (sequence, team's heads, row tile) unit costs ceil(L / 128) tiles; the line
+//    of all units' tiles is cut into equal parts, one per team (one CTA per SM), whatever
+//    the lengths.  A unit that lies in one part is finished there; others leave fp32
+//    partial states, two at most per CTA, that paged_merge_kernel joins in order.  No
+//    atomics: results do not depend on timing.
+//  * Warp roles: 0 MMA issuer, 1 page lookup, 2 K loader, 3 V loader, 4-7 softmax and
+//    epilogue.  The lookup warp turns tiles into rows of the cache, up to eight tiles
+//    ahead, in a ring that the loaders copy from, and fetches the rows' scale bytes: as the
+//    aligned words that hold them (asynchronous copies have no smaller size), cut out by
+//    the softmax.
+//  * Every role is a small loop: one warp of each runs per scheduler, and with the loaders'
+//    loops unrolled (2000 instructions each) two fifths of all stalls were for instructions
+//    not yet fetched (64 requests, 8 key heads: 499 us).
+//  * Few waits: the issue order Q K^T of tile c + 1, then P V of tile c, makes the scores'
+//    barrier of a tile imply that the products of two tiles before have read their
+//    weights, and the weights' barrier that the scores have been read.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -56,8 +72,9 @@ namespace fa {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 256;
 constexpr int kTile = 128;  // keys per tile
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;  // past the sequence's end
 
 // Exponent offset and threshold of the running maximum, log2 units.  8 bit: weights
 // up to 2^(7 + 1) use e4m3's range (448) and leave the second piece a floor of
@@ -71,21 +88,31 @@ struct SoftmaxRange {
 template <int N, bool kQ8>
 struct PagedLayout {
   static constexpr int kSlotBytes = kTile * 128 * (kQ8 ? 1 : 2);  // one K or V tile
-  static constexpr int kSlots = (kQ8 ? 2 : 1) * (N == 64 ? 5 : 6);
+  static constexpr int kSlots = kQ8 ? (N == 64 ? 9 : (N == 32 ? 11 : 12)) : (N == 64 ? 5 : 6);  // what fits
   static constexpr int kRowBlock = N * 128;      // one 128-byte column block of the N rows
   static constexpr int kOffQ = kSlots * kSlotBytes;  // two e4m3 pieces, or two 64-dim blocks
-  static constexpr int kOffP = kOffQ + 2 * kRowBlock;  // double buffer of two pieces / 64-key blocks
+  static constexpr int kOffP = kOffQ + 2 * kRowBlock;  // double buffer of two e4m3 pieces, or of bf16
   static constexpr int kOffBar = kOffP + 4 * kRowBlock;
-  // kv_full[S], kv_empty[S], q_full, s_full[2], s_free[2], p_full[2], p_free[2]
-  static constexpr int kNumBars = 2 * kSlots + 9;
+  // kv_full[S], kv_empty[S], q_full, s_full[2], p_full[2], p_done, rows_full[R], rows_empty[R]
+  static constexpr int kRing = 8;  // tiles that the page lookup may be ahead
+  static constexpr int kNumBars = 2 * kSlots + 6 + 2 * kRing;
   static constexpr int kOffMisc = kOffBar + ((kNumBars * 8 + 15) & ~15);
   static constexpr int kOffRows = kOffMisc + 64;
   // per row: factor, limit, threshold, reference, rescale, running max, output row; per warp and row: two sums
-  static constexpr int kSmemBytes = kOffRows + 7 * N * 4 + 8 * N * 4 + 1024;  // + alignment slack
-  static constexpr uint32_t kTmemCols = N == 16 ? 64 : (N == 32 ? 128 : 256);  // S, S, O: 3 N
+  static constexpr int kOffRing = (kOffRows + 15 * N * 4 + 15) & ~15;  // per tile: 128 cache rows
+  static constexpr int kOffTile = kOffRing + kRing * kTile * 4;         // per tile: head (or pair), -1: no more tiles
+  // per tile and key: the words of K's and V's scale bytes, two each when two heads may
+  // lie in different words
+  static constexpr int kOffScales = kOffTile + kRing * 4;
+  static constexpr int kSmemBytes = kOffScales + (kQ8 ? kRing * kTile * 16 : 0) + 1024;  // + alignment slack
+  static_assert(kSmemBytes <= 232448, "shared memory of one SM");
+  static constexpr int kCols = kQ8 ? 2 * N : N;  // columns of a product: rows, in 8 bits two pieces of each
+  static constexpr uint32_t kTmemCols = (N == 16 ? 64 : (N == 32 ? 128 : 256)) * (kQ8 ? 2 : 1);  // S, S, O
 };
 
 struct PagedArgs {
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
   const __nv_bfloat16* q;
   long long q_stride;  // elements between tokens
   __nv_bfloat16* o;
@@ -97,9 +124,11 @@ struct PagedArgs {
   const uint8_t* k_scales;
   const uint8_t* v_scales;
   int* status;
-  int B, Hq, Hkv, G, groups;  // groups: key heads (d = 128) or pairs of them (d = 64)
+  int B, Hq, Hkv, G;
+  int team, teams, sets;  // CTAs (key heads, or pairs of them when d = 64) of a team, teams, teams' worths of heads
   int total_q, max_q, max_k;
-  int num_pages, page_size, max_pages, box_rows;
+  int num_pages, page_size, max_pages;
+  uint32_t page_mul, page_shift;  // division by page_size
   int causal;
   float scale_log2;
   int4* meta;       // [CTAs]: parts of the unit that begins in this CTA and ends in a later one
@@ -111,9 +140,19 @@ struct PagedArgs {
   unsigned long long timeout_ns;
 };
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns) {
+// Bounded waits, false also when another role of the CTA has given up.  A phase that is
+// complete at the first look costs no more than that look (every lane's, so that nothing
+// has to be handed over).
+__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns,
+                                            volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, timeout_ns) && !*abort_flag;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns,
+                                          volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   bool ok = true;
-  if (lane_id() == 0) ok = mbar_wait(bar, parity, timeout_ns);
+  if (lane_id() == 0) ok = mbar_wait(bar, parity, timeout_ns) && !*abort_flag;
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
@@ -153,11 +192,11 @@ __device__ __forceinline__ int row_tiles(const PagedArgs& a, int nq) {
 // Tiles of one unit of a sequence (one, fully masked, when it has no key).
 __device__ __forceinline__ int unit_tiles(int lk) { return max(1, (lk + kTile - 1) / kTile); }
 
-// This CTA's stretch [pos, end) of the line of tiles, as pieces of units.
+// This CTA's (its team's) stretch [pos, end) of the line of tiles, as pieces of units.
 struct Work {
   long long pos, end, total;
   int b, off;  // sequence of pos, and pos's place among its tiles
-  int ctas;    // CTAs that have a stretch
+  int teams;   // teams that have a stretch
 };
 struct Piece {
   int b, hg, rt, t0, t1, tiles;
@@ -170,12 +209,13 @@ __device__ __forceinline__ bool next_piece(const PagedArgs& a, Work& w, Piece& p
     p.s = seq_info(a, w.b);
     const int rts = row_tiles<N, D>(a, p.s.nq);
     p.tiles = unit_tiles(p.s.lk);
-    const int cost = rts * a.groups * p.tiles;
+    const int cost = rts * a.sets * p.tiles;
     if (w.off < cost) {
       const int u = w.off / p.tiles;
       p.b = w.b;
-      p.hg = u / rts;
-      p.rt = u - p.hg * rts;
+      const int set = u / rts;
+      p.hg = set * a.team + (int)blockIdx.x % a.team;
+      p.rt = u - set * rts;
       p.t0 = w.off - u * p.tiles;
       p.t1 = (int)min((long long)p.tiles, p.t0 + (w.end - w.pos));
       w.pos += p.t1 - p.t0;
@@ -187,6 +227,13 @@ __device__ __forceinline__ bool next_piece(const PagedArgs& a, Work& w, Piece& p
   return false;
 }
 
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, "Division by
+// Invariant Integers using Multiplication", 1994): s = ceil(log2 d), m = floor(2^32 (2^s - d)
+// / d) + 1, n / d = (hi(m n) + n) >> s.
+__device__ __forceinline__ int page_index(const PagedArgs& a, int n) {
+  return (int)((__umulhi(a.page_mul, (uint32_t)n) + (uint32_t)n) >> a.page_shift);
+}
+
 // Run by one warp: the line's length and where this CTA's stretch begins.
 template <int N, int D>
 __device__ __forceinline__ Work find_work(const PagedArgs& a) {
@@ -195,7 +242,7 @@ __device__ __forceinline__ Work find_work(const PagedArgs& a) {
   auto cost_of = [&](int b) {
     if (b >= a.B) return 0;
     const SeqInfo s = seq_info(a, b);
-    return row_tiles<N, D>(a, s.nq) * a.groups * unit_tiles(s.lk);
+    return row_tiles<N, D>(a, s.nq) * a.sets * unit_tiles(s.lk);
   };
   long long total = 0;
   for (int b = lane; b < a.B; b += 32) {
@@ -205,13 +252,14 @@ __device__ __forceinline__ Work find_work(const PagedArgs& a) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   w.total = total;
-  w.ctas = (int)min((long long)gridDim.x, total);
+  w.teams = (int)min((long long)a.teams, total);
+  const int team = blockIdx.x / a.team;
   w.b = 0;
   w.off = 0;
   w.pos = w.end = 0;
-  if ((int)blockIdx.x >= w.ctas) return w;
-  w.pos = total * blockIdx.x / w.ctas;
-  w.end = total * (blockIdx.x + 1) / w.ctas;
+  if (team >= w.teams) return w;
+  w.pos = total * team / w.teams;
+  w.end = total * (team + 1) / w.teams;
   long long before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int mine = cost_of(b0 + lane);
@@ -231,17 +279,6 @@ __device__ __forceinline__ Work find_work(const PagedArgs& a) {
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
   return w;
-}
-
-// Row of the flattened pages that holds key j of sequence b (a page outside the cache is
-// recorded and read as page 0).
-__device__ __forceinline__ int cache_row(const PagedArgs& a, int b, int j) {
-  int page = __ldg(a.table + (size_t)b * a.max_pages + j / a.page_size);
-  if (page < 0 || page >= a.num_pages) {
-    atomicExch(a.status, kStatusBadArg);
-    page = 0;
-  }
-  return page * a.page_size + j % a.page_size;
 }
 
 __device__ __forceinline__ float redux_max(float x) {
@@ -297,7 +334,7 @@ __device__ __forceinline__ float warp_sums(float (&v)[N]) {
 
 template <int N, bool kQ8, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
+    paged_kernel(const PagedArgs a) {
   using L = PagedLayout<N, kQ8>;
   using R = SoftmaxRange<kQ8>;
   constexpr int kHeadRows = head_rows<N, D>();
@@ -308,9 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* kv_empty = bars + L::kSlots;
   uint64_t* q_full = bars + 2 * L::kSlots;
   uint64_t* s_full = q_full + 1;
-  uint64_t* s_free = q_full + 3;
-  uint64_t* p_full = q_full + 5;
-  uint64_t* p_free = q_full + 7;
+  uint64_t* p_full = q_full + 3;
+  uint64_t* p_done = q_full + 5;
+  uint64_t* rows_full = q_full + 6;
+  uint64_t* rows_empty = rows_full + L::kRing;
+  uint32_t* ring_rows = reinterpret_cast<uint32_t*>(smem + L::kOffRing);
+  volatile int* ring_tile = reinterpret_cast<volatile int*>(smem + L::kOffTile);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
   // a softmax wait gave up: set before the tile's first barrier or after its last, read between
@@ -319,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(sizeof(Work) <= 48, "the stretch fits its place");
   const uint32_t warp = warp_id(), lane = lane_id();
 
-  if (warp == 2) {
+  if (warp == 4) {
     const Work w = find_work<N, D>(a);
     if (lane == 0) {
       *work = w;
@@ -328,24 +368,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(kv_full + s, 1);
+      mbar_init(kv_full + s, 32);  // the copying lanes
       mbar_init(kv_empty + s, 1);
     }
     mbar_init(q_full, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(s_free + i, 4);
       mbar_init(p_full + i, 4);
-      mbar_init(p_free + i, 1);
+    }
+    mbar_init(p_done, 1);
+    for (int i = 0; i < L::kRing; ++i) {
+      mbar_init(rows_full + i, kQ8 ? 33 : 1);  // the lookup warp, in 8 bits also its lanes' scale copies
+      mbar_init(rows_empty + i, kQ8 ? 6 : 2);  // both loaders; the softmax warps, which need a row's place for its scales
     }
     *abort_flag = 0;
     *group_dead = 0;
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == 1) {
+  if (warp == 0) {
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
@@ -359,91 +400,155 @@ __global__ void __launch_bounds__(kThreads, 1)
     atomicCAS(a.status, 0, kStatusTimeout);
   };
 
-  if (warp == 0) {
-    // -------------------------------------------------------------------- TMA producer
-    const int boxes = kTile / a.box_rows;
-    const uint32_t box_bytes = (uint32_t)a.box_rows * 128 * (kQ8 ? 1 : 2);
-    uint32_t g = 0;
-    bool ok = true;
+  if (warp == 1) {
+    // -------------------------------------------------------------------- page lookup
     Piece p;
-    while (ok && next_piece<N, D>(a, w, p)) {
-      for (int t = p.t0; ok && t < p.t1; ++t) {
-        const int key0 = t * kTile;
-        const int valid = max(0, min(boxes, (p.s.lk - key0 + a.box_rows - 1) / a.box_rows));
-        for (int kv = 0; ok && kv < 2; ++kv, ++g) {
-          const uint32_t slot = g % L::kSlots;
-          if (lane == 0) {
-            ok = mbar_wait(kv_empty + slot, ((g / L::kSlots) & 1) ^ 1, a.timeout_ns) && !*abort_flag;
-            if (!ok)
-              give_up();
-            else if (valid > 0)
-              mbar_arrive_expect_tx(kv_full + slot, valid * box_bytes);
-            else
-              mbar_arrive(kv_full + slot);
-          }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;
-          uint8_t* dst = smem + slot * L::kSlotBytes;
-          const CUtensorMap* map = kv ? &tmV : &tmK;
-          for (int i = lane; i < valid; i += 32) {
-            const int row = cache_row(a, p.b, key0 + i * a.box_rows);
-            uint8_t* to = dst + i * a.box_rows * 128;
-            if constexpr (kQ8) {
-              tma_load_2d(to, map, kv_full + slot, p.hg * 128, row);
-            } else {
-              const int x = p.hg * 128;
-              tma_load_2d(to, map, kv_full + slot, x, row);
-              tma_load_2d(to + kTile * 128, map, kv_full + slot, x + 64, row);
+    uint32_t c = 0;
+    bool ok = true;
+    const long long scale_bytes = (long long)a.num_pages * a.page_size * a.Hkv;
+    auto publish = [&](const int(&page)[4], int key0, int lk, int tile) {
+      const uint32_t at = c % L::kRing;
+      ok = warp_wait(rows_empty + at, ((c / L::kRing) & 1) ^ 1, a.timeout_ns, abort_flag);
+      if (!ok) return;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = key0 + (int)lane + 32 * i;
+        int pg = page[i];
+        if (pg < 0 || pg >= a.num_pages) {  // never read outside the cache
+          atomicExch(a.status, kStatusBadArg);
+          pg = 0;
+        }
+        const uint32_t row = (uint32_t)(pg * a.page_size + (key - page_index(a, key) * a.page_size));
+        ring_rows[at * kTile + lane + 32 * i] = key < lk ? row : kNoRow;
+        if constexpr (kQ8) {
+          if (key < lk) {
+            // the words that hold the key's scale bytes (never past the arrays' ends)
+            const uint32_t to = smem_u32(smem + L::kOffScales) + (at * kTile + lane + 32 * i) * 16;
+            const long long o = ((long long)row * a.Hkv + (D == 64 ? 2 : 1) * tile) & ~3LL;
+            const int n0 = (int)min(4LL, scale_bytes - o), n1 = (int)max(0LL, min(4LL, scale_bytes - o - 4));
+            cp_async4(to, a.k_scales + o, n0);
+            cp_async4(to + 8, a.v_scales + o, n0);
+            if constexpr (D == 64) {
+              cp_async4(to + 4, a.k_scales + (n1 ? o + 4 : o), n1);
+              cp_async4(to + 12, a.v_scales + (n1 ? o + 4 : o), n1);
             }
           }
-          __syncwarp();
         }
       }
+      if (lane == 0) ring_tile[at] = tile;
+      if constexpr (kQ8) cp_async_arrive(rows_full + at);
+      mbar_arrive_warp(rows_full + at);
+      ++c;
+    };
+    while (ok && next_piece<N, D>(a, w, p)) {
+      const int32_t* table = a.table + (size_t)p.b * a.max_pages;
+      int page[4], next[4];
+      auto look_up = [&](int t, int(&x)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = t * kTile + (int)lane + 32 * i;
+          x[i] = t < p.t1 && key < p.s.lk ? __ldg(table + page_index(a, key)) : 0;
+        }
+      };
+      look_up(p.t0, next);
+#pragma unroll 1
+      for (int t = p.t0; ok && t < p.t1; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) page[i] = next[i];
+        look_up(t + 1, next);
+        publish(page, t * kTile, p.s.lk, p.hg);
+      }
     }
-    if (!ok && lane == 0)  // copies already issued land before the CTA retires
-      for (uint32_t i = g > L::kSlots ? g - L::kSlots : 0; i < g; ++i)
-        (void)mbar_wait(kv_full + (i % L::kSlots), (i / L::kSlots) & 1, a.timeout_ns);
-  } else if (warp == 1) {
+    if (ok) {
+      const int none[4] = {0, 0, 0, 0};
+      publish(none, 0, 0, -1);
+    }
+    if (!ok && lane == 0) give_up();
+    if constexpr (kQ8) cp_async_wait_all();
+  } else if (warp == 2 || warp == 3) {
+    // -------------------------------------------------------------------- K and V loaders
+    const bool is_v = warp == 3;
+    const uint32_t row_bytes = (uint32_t)a.Hkv * D * (kQ8 ? 1 : 2);
+    const int chunk = lane & 7, sub = lane >> 3;  // 16-byte chunk of a 128-byte row, key of four
+    const uint32_t to0 = sub * 128 + ((chunk ^ sub) << 4), to1 = (sub + 4) * 128 + ((chunk ^ (sub + 4)) << 4);
+    const uint32_t ring = smem_u32(ring_rows);
+    bool ok = true;
+    for (uint32_t c = 0;; ++c) {
+      const uint32_t at = c % L::kRing, g = 2 * c + is_v, slot = g % L::kSlots;
+      ok = warp_wait(rows_full + at, (c / L::kRing) & 1, a.timeout_ns, abort_flag);
+      if (!ok) break;
+      const int hg = ring_tile[at];
+      if (hg < 0) break;
+      ok = warp_wait(kv_empty + slot, ((g / L::kSlots) & 1) ^ 1, a.timeout_ns, abort_flag);
+      if (!ok) break;
+      // a pair of 64-dim heads whose second is past the last has no bytes for it
+      const bool lone = D == 64 && 2 * hg + 1 >= a.Hkv;
+      const uint8_t* src = (is_v ? a.v_pages : a.k_pages) + hg * (kQ8 ? 128 : 256) + chunk * 16;
+      uint32_t dst = smem_u32(smem + slot * L::kSlotBytes);
+      uint32_t rows = ring + (at * kTile + sub) * 4;
+      const bool mine = !(kQ8 && lone && chunk >= 4);
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i, dst += 4096, rows += 128) {
+        uint32_t rw[8];  // of keys 32 i + 4 j + sub
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rw[j] = ld_shared_u32(rows + 16 * j);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool have = rw[j] != kNoRow && mine;
+          const uint8_t* from = src + (uint64_t)(have ? rw[j] : 0u) * row_bytes;
+          const uint32_t to = dst + (j / 2) * 1024 + (j % 2 ? to1 : to0);
+          cp_async16_or_zero(to, from, have);
+          if constexpr (!kQ8) cp_async16_or_zero(to + kTile * 128, lone ? from : from + 128, have && !lone);
+        }
+      }
+      mbar_arrive_warp(rows_empty + at);
+      cp_async_arrive(kv_full + slot);
+    }
+    if (!ok) {
+      if (lane == 0) give_up();
+      cp_async_wait_all();  // copies already issued land before the CTA retires
+    }
+  } else if (warp == 0) {
     // -------------------------------------------------------------------- MMA issuer
     if (lane == 0) {
-      constexpr uint32_t kIdescS = kQ8 ? idesc_e4m3_f32(128, N, false, false) : idesc_bf16_f32(128, N, false, false);
-      constexpr uint32_t kIdescO = kQ8 ? idesc_e4m3_f32(128, N, true, false) : idesc_bf16_f32(128, N, true, false);
+      constexpr uint32_t kIdescS = kQ8 ? idesc_e4m3_f32(128, 2 * N, false, false) : idesc_bf16_f32(128, N, false, false);
+      constexpr uint32_t kIdescO = kQ8 ? idesc_e4m3_f32(128, 2 * N, true, true) : idesc_bf16_f32(128, N, true, true);
       const uint32_t base = smem_u32(smem);
       const SDesc k_desc = sdesc_make(base, 16, 1024);                     // K-major keys
       const SDesc v_desc = sdesc_make(base, kQ8 ? 16 : 16384, 1024);       // dims along M: MN-major
       const SDesc q_desc = sdesc_make(base + L::kOffQ, 16, 1024);
-      const SDesc p_desc = sdesc_make(base + L::kOffP, 16, 1024);
+      const SDesc p_desc = sdesc_make_mn_plain(base + L::kOffP, 128, kTile * 16);  // rows along N: MN-major
       constexpr uint32_t kSlot16 = L::kSlotBytes / 16, kBlock16 = L::kRowBlock / 16;
-      const uint32_t tO = tmem + 2 * N;
+      const uint32_t tO = tmem + 2 * L::kCols;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && (!mbar_wait(bar, parity, a.timeout_ns) || *abort_flag)) {
+        if (ok && !thread_wait(bar, parity, a.timeout_ns, abort_flag)) {
           give_up();
           ok = false;
         }
         return ok;
       };
-      auto product = [&](uint32_t d, SDesc x, uint32_t x_step, SDesc y, uint32_t idesc, bool accumulate) {
-        // 8 bit: 4 steps of 32, for each of y's two pieces; bf16: 8 steps of 16 over two blocks
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t xo = kQ8 ? (i & 3) * x_step : (x_step == 2 ? (i >> 2) * 1024 + (i & 3) * 2 : i * x_step);
-          const uint64_t xd = sdesc_at(x, xo), yd = sdesc_at(y, (i >> 2) * kBlock16 + (i & 3) * 2);
-          if constexpr (kQ8)
-            umma_ss_f8(d, xd, yd, idesc, (accumulate || i > 0) ? 1u : 0u);
-          else
-            umma_ss(d, xd, yd, idesc, (accumulate || i > 0) ? 1u : 0u);
-        }
+      // one step of a product: 32 deep in 8 bits, 16 in bf16
+      auto step = [&](uint32_t d, uint64_t x, uint64_t y, uint32_t idesc, bool accumulate) {
+        if constexpr (kQ8)
+          umma_ss_f8(d, x, y, idesc, accumulate ? 1u : 0u);
+        else
+          umma_ss(d, x, y, idesc, accumulate ? 1u : 0u);
       };
       uint32_t c = 0, piece = 0;  // tiles and pieces so far
       auto pv = [&](uint32_t x, bool accumulate) {
         const uint32_t slot = (2 * x + 1) % L::kSlots;
         if (!wait(p_full + (x & 1), (x >> 1) & 1)) return;
         if (!wait(kv_full + slot, ((2 * x + 1) / L::kSlots) & 1)) return;
+        fence_proxy_async_smem();  // the loaders' copies, before the tensor core reads them
         tc_fence_after();
-        product(tO, SDesc{v_desc.lo + slot * kSlot16, v_desc.hi}, kQ8 ? 256 : 128,
-                SDesc{p_desc.lo + (x & 1) * 2 * kBlock16, p_desc.hi}, kIdescO, accumulate);
-        umma_commit(p_free + (x & 1));
+        const SDesc v = SDesc{v_desc.lo + slot * kSlot16, v_desc.hi};
+        const SDesc pd = SDesc{p_desc.lo + (x & 1) * 2 * kBlock16, p_desc.hi};
+        // keys 32 i .. or 16 i ..
+#pragma unroll
+        for (int i = 0; i < (kQ8 ? 4 : 8); ++i)
+          step(tO, sdesc_at(v, i * (kQ8 ? 256 : 128)), sdesc_at(pd, i * (kQ8 ? 32 : 16)), kIdescO, accumulate || i > 0);
+        umma_commit(p_done);
         umma_commit(kv_empty + slot);
       };
       Piece p;
@@ -454,9 +559,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; ok && t < n; ++t, ++c) {
           const uint32_t slot = (2 * c) % L::kSlots;
           if (!wait(kv_full + slot, ((2 * c) / L::kSlots) & 1)) break;
-          if (c >= 2 && !wait(s_free + (c & 1), ((c >> 1) - 1) & 1)) break;
+          fence_proxy_async_smem();
           tc_fence_after();
-          product(tmem + (c & 1) * N, SDesc{k_desc.lo + slot * kSlot16, k_desc.hi}, 2, q_desc, kIdescS, false);
+          const SDesc k = SDesc{k_desc.lo + slot * kSlot16, k_desc.hi};
+          // dims 32 i .. or 16 i .. of two 64-dim blocks
+#pragma unroll
+          for (int i = 0; i < (kQ8 ? 4 : 8); ++i)
+            step(tmem + (c & 1) * L::kCols, sdesc_at(k, (i >> 2) * 1024 + (i & 3) * 2),
+                 sdesc_at(q_desc, (i >> 2) * kBlock16 + (i & 3) * 2), kIdescS, i > 0);
           umma_commit(s_full + (c & 1));
           umma_commit(kv_empty + slot);
           if (t > 0) pv(c - 1, t > 1);
@@ -468,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------------- softmax and epilogue
     const uint32_t quarter = warp & 3;
     const int r = quarter * 32 + lane;         // key of the tile, then dim of O
-    const int tid = threadIdx.x - 64;          // 0 .. 127
+    const int tid = threadIdx.x - 128;         // 0 .. 127
     const uint32_t lanes = (quarter * 32) << 16;
     float* factor = reinterpret_cast<float*>(smem + L::kOffRows);  // of the scores: scale, log2 e, Q's scale
     int* limit = reinterpret_cast<int*>(factor + N);               // first key that the row does not see
@@ -480,12 +590,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* wred = factor + 7 * N;    // [4][N] maxima, then sums
     float* wred2 = wred + 4 * N;
     uint32_t c = 0;
+    // the N rows of a product, pieces added up
+    auto ld_rows = [&](uint32_t at, float(&x)[N]) {
+      if constexpr (kQ8) {
+        float second[N];
+        tmem_ld_cols2<N>(at, at + N, x, second);
+#pragma unroll
+        for (int n = 0; n < N; ++n) x[n] += second[n];
+      } else {
+        tmem_ld_cols<N>(at, x);
+      }
+    };
     // A wait that gives up does not leave at once: the group's barriers need all four
     // warps, so the warp goes on (waiting no more) to the next place where all leave
     // together.
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok && (!warp_wait(bar, parity, a.timeout_ns) || *abort_flag)) {
+      if (ok && !warp_wait(bar, parity, a.timeout_ns, abort_flag)) {
         if (lane == 0) {
           give_up();
           *group_dead = 1;
@@ -570,6 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive_warp(q_full);
       named_bar_sync(1, 128);
+      // rows of each head that there are (the others' columns hold nothing of use)
+      const int live = min(kHeadRows, p.s.nq * a.G - p.rt * kHeadRows);
       // keys that every row of the tile sees: [0, all_see)
       const int first_token = (p.rt * kHeadRows) / a.G;
       const int all_see = a.causal ? max(0, min(p.s.lk, p.s.lk - p.s.nq + first_token + 1)) : p.s.lk;
@@ -584,39 +707,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < tiles; ++t, ++c) {
         const int key = (p.t0 + t) * kTile + r;
         const int tile_end = (p.t0 + t + 1) * kTile;
-        // the key's scales (two heads' when d = 64), while its scores are made
-        float kf[2] = {1.f, 1.f}, ve[2] = {0.f, 0.f}, vinv[2] = {1.f, 1.f};
-        if constexpr (kQ8) {
-          if (key < p.s.lk) {
-            const size_t at = (size_t)cache_row(a, p.b, key) * a.Hkv;
-#pragma unroll
-            for (int h = 0; h < (D == 64 ? 2 : 1); ++h) {
-              const int hk = D == 64 ? 2 * p.hg + h : p.hg;
-              if (hk < a.Hkv) {
-                kf[h] = __uint_as_float((uint32_t)__ldg(a.k_scales + at + hk) << 23);
-                const int e = (int)__ldg(a.v_scales + at + hk) - 127;
-                ve[h] = (float)e;
-                vinv[h] = __uint_as_float((uint32_t)(127 - e) << 23);
-              }
-            }
-          }
-        }
         wait(s_full + (c & 1), (c >> 1) & 1);
         tc_fence_after();
+        float kf[2] = {1.f, 1.f}, ve[2] = {0.f, 0.f}, vinv[2] = {1.f, 1.f};  // the key's scales, two heads' when d = 64
+        if constexpr (kQ8) {
+          const uint32_t at = c % L::kRing, rw = ring_rows[at * kTile + r];
+          const uint4 words = reinterpret_cast<const uint4*>(smem + L::kOffScales)[at * kTile + r];
+          mbar_arrive_warp(rows_empty + at);
+          // byte of the head in its word, and the pair's second head's after it
+          const uint32_t cut = ((rw * (uint32_t)a.Hkv + (D == 64 ? 2 : 1) * p.hg) & 3u) * 8;
+          uint32_t kb = D == 64 ? __funnelshift_r(words.x, words.y, cut) : words.x >> cut;
+          uint32_t vb = D == 64 ? __funnelshift_r(words.z, words.w, cut) : words.z >> cut;
+          if (rw == kNoRow) kb = vb = 0x7F7Fu;  // 2^0
+#pragma unroll
+          for (int h = 0; h < (D == 64 ? 2 : 1); ++h) {
+            kf[h] = __uint_as_float(((kb >> (8 * h)) & 0xFFu) << 23);
+            const int e = (int)((vb >> (8 * h)) & 0xFFu) - 127;
+            ve[h] = (float)e;
+            vinv[h] = __uint_as_float((uint32_t)(127 - e) << 23);
+          }
+        }
         float y[N];
-        tmem_ld_cols<N>(tmem + lanes + (c & 1) * N, y);
-        tc_fence_before();
-        mbar_arrive_warp(s_free + (c & 1));
+        ld_rows(tmem + lanes + (c & 1) * L::kCols, y);
         const bool masked = tile_end > all_see;
         bool over = !ok;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const int h = (D == 64 && n >= kHeadRows) ? 1 : 0;
-          float x = y[n] * factor[n];
-          if constexpr (kQ8) x = fmaf(x, kf[h], ve[h]);
-          if (masked && key >= limit[n]) x = -INFINITY;
-          y[n] = x;
-          over |= x > thresh[n];
+        for (int n0 = 0; n0 < N; n0 += 4) {
+          const int h = (D == 64 && n0 >= kHeadRows) ? 1 : 0;
+          if (n0 - h * kHeadRows < live) {
+#pragma unroll
+            for (int n = n0; n < n0 + 4; ++n) {
+              float x = y[n] * factor[n];
+              if constexpr (kQ8) x = fmaf(x, kf[h], ve[h]);
+              if (masked && key >= limit[n]) x = -INFINITY;
+              y[n] = x;
+              over |= x > thresh[n];
+            }
+          }
         }
         if (any_of_group(over)) {
           // some key exceeds its row's running maximum: the tile's maximum of every row
@@ -655,58 +782,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (!kQ8) lr[n] *= alpha[n];
           }
           if (t > 0) {  // O holds earlier tiles: rescale it once the last product is in
-            wait(p_free + ((c - 1) & 1), ((c - 1) >> 1) & 1);
+            wait(p_done, (c - 1) & 1);
             tc_fence_after();
             uint32_t o[16];
 #pragma unroll 1
-            for (int n0 = 0; n0 < N; n0 += 16) {
-              tmem_ld16(tmem + lanes + 2 * N + n0, o);
+            for (int n0 = 0; n0 < L::kCols; n0 += 16) {
+              tmem_ld16(tmem + lanes + 2 * L::kCols + n0, o);
               tmem_ld_wait16(o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[n0 + i]);
-              tmem_st16(tmem + lanes + 2 * N + n0, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[n0 % N + i]);
+              tmem_st16(tmem + lanes + 2 * L::kCols + n0, o);
             }
             tmem_st_wait();
           }
         }
-        // weights; the buffer is free once the product of two tiles ago has read it
-        if (c >= 2) wait(p_free + (c & 1), ((c >> 1) - 1) & 1);
-        const uint32_t pbuf = smem_u32(smem + L::kOffP) + (c & 1) * 2 * L::kRowBlock;
+        // weights, into the buffer that the product of two tiles ago has read
+        // 16 bytes of rows at a time for this key; rows past the chunk's last are left out
+        const uint32_t pbuf = smem_u32(smem + L::kOffP) + (c & 1) * 2 * L::kRowBlock + r * 16;
+        constexpr int kGroup = kQ8 ? 16 : 8;
 #pragma unroll
-        for (int n = 0; n < N; n += 2) {
-          const int h = (D == 64 && n >= kHeadRows) ? 1 : 0;
-          const float2 pw = make_float2(ex2(y[n] - ref[n]), ex2(y[n + 1] - ref[n + 1]));
-          l[n] = fmaf(pw.x, vinv[h], l[n]);
-          l[n + 1] = fmaf(pw.y, vinv[h], l[n + 1]);
-          if constexpr (kQ8) {
-            const uint32_t p1 = to_e4m3x2(pw.x, pw.y);
-            const float2 b1 = of_e4m3x2(p1);
-            const uint32_t p2 = to_e4m3x2(pw.x - b1.x, pw.y - b1.y);
-            const uint32_t at0 = pbuf + n * 128 + (((r >> 4) ^ (n & 7)) << 4) + (r & 15);
-            const uint32_t at1 = pbuf + (n + 1) * 128 + (((r >> 4) ^ ((n + 1) & 7)) << 4) + (r & 15);
-            st_shared_u8(at0, p1);
-            st_shared_u8(at1, p1 >> 8);
-            st_shared_u8(at0 + L::kRowBlock, p2);
-            st_shared_u8(at1 + L::kRowBlock, p2 >> 8);
-          } else {
-            const uint32_t k2 = pack_bf16x2(pw.x, pw.y);
-            lr[n] += __uint_as_float(k2 << 16);
-            lr[n + 1] += __uint_as_float(k2 & 0xFFFF0000u);
-            const uint32_t block = pbuf + (r >> 6) * L::kRowBlock, chunk = (r & 63) >> 3, in = (r & 7) * 2;
-            st_shared_u16(block + n * 128 + ((chunk ^ (n & 7)) << 4) + in, k2);
-            st_shared_u16(block + (n + 1) * 128 + ((chunk ^ ((n + 1) & 7)) << 4) + in, k2 >> 16);
-          }
-        }
-        if (tile_end > p.s.lk) {
-          // V rows past the sequence's end: whatever the slot or the page holds there
-          // becomes zero
-          const uint32_t slot = (2 * c + 1) % L::kSlots;
-          wait(kv_full + slot, ((2 * c + 1) / L::kSlots) & 1);
-          if (key >= p.s.lk) {
-            const uint32_t at = smem_u32(smem + slot * L::kSlotBytes) + r * 128;
+        for (int n0 = 0; n0 < N; n0 += kGroup) {
+          uint32_t p1[4] = {0, 0, 0, 0}, p2[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < (kQ8 ? 8 : 16); ++i) st_shared_v4(at + (i >> 3) * kTile * 128 + (i & 7) * 16, 0, 0, 0, 0);
+          for (int i = 0; i < kGroup; i += 4) {
+            const int n = n0 + i;
+            const int h = (D == 64 && n >= kHeadRows) ? 1 : 0;
+            if (n - h * kHeadRows < live) {
+              float pw[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                pw[j] = ex2(y[n + j] - ref[n + j]);
+                l[n + j] = fmaf(pw[j], vinv[h], l[n + j]);
+              }
+              if constexpr (kQ8) {
+                const uint32_t lo = to_e4m3x2(pw[0], pw[1]), hi = to_e4m3x2(pw[2], pw[3]);
+                const float2 bl = of_e4m3x2(lo), bh = of_e4m3x2(hi);
+                p1[i / 4] = lo | (hi << 16);
+                p2[i / 4] = to_e4m3x2(pw[0] - bl.x, pw[1] - bl.y) | (to_e4m3x2(pw[2] - bh.x, pw[3] - bh.y) << 16);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                  const uint32_t k2 = pack_bf16x2(pw[j], pw[j + 1]);
+                  p1[(i + j) / 2] = k2;
+                  lr[n + j] += __uint_as_float(k2 << 16);
+                  lr[n + j + 1] += __uint_as_float(k2 & 0xFFFF0000u);
+                }
+              }
+            }
           }
+          const uint32_t at = pbuf + (n0 / kGroup) * kTile * 16;
+          st_shared_v4(at, p1[0], p1[1], p1[2], p1[3]);
+          if constexpr (kQ8) st_shared_v4(at + L::kRowBlock, p2[0], p2[1], p2[2], p2[3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -714,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- epilogue: all products of the piece are in (a group that broke off has ok =
       // false in every warp and leaves here)
-      if (ok) wait(p_free + ((c - 1) & 1), ((c - 1) >> 1) & 1);
+      if (ok) wait(p_done, (c - 1) & 1);
       if (any_of_group(!ok)) break;
       tc_fence_after();
       constexpr int kSum = N < 32 ? N : 32;
@@ -736,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       named_bar_sync(1, 128);
       float o[N];
-      tmem_ld_cols<N>(tmem + lanes + 2 * N, o);
+      ld_rows(tmem + lanes + 2 * L::kCols, o);
       const bool whole = p.t0 == 0 && p.t1 == p.tiles;
       if (whole) {
 #pragma unroll
@@ -765,9 +891,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.t0 == 0) a.part_rows[(size_t)blockIdx.x * N + tid] = out_row[tid];
         }
         if (p.t0 == 0 && tid == 0) {
-          // the CTA that has the unit's last tile
+          // parts up to the team that has the unit's last tile
           const long long last = w.pos - p.t1 + p.tiles - 1;
-          a.meta[blockIdx.x] = make_int4((int)(((last + 1) * w.ctas - 1) / w.total) - (int)blockIdx.x + 1, 0, 0, 0);
+          a.meta[blockIdx.x] =
+              make_int4((int)(((last + 1) * w.teams - 1) / w.total) - (int)blockIdx.x / a.team + 1, 0, 0, 0);
         }
       }
       named_bar_sync(1, 128);  // the rows' places are written again for the next piece
@@ -776,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
@@ -784,7 +911,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partial states of the unit that begins in attention CTA blockIdx.x (none:
 // nothing to do), a warp per row: with M the largest reference, every part's sums and
-// O count 2^(m - M).  Part 0 is that CTA's slot 1, part i the slot 0 of CTA + i.
+// O count 2^(m - M).  Part 0 is that CTA's slot 1, part i the slot 0 of the same member of
+// the i-th team after its.
 template <int N, int D>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
   const int cta = blockIdx.x, parts = a.meta[cta].x;
@@ -792,7 +920,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
   const int n = blockIdx.y * 4 + warp_id(), lane = lane_id();
   const int row = a.part_rows[(size_t)cta * N + n];
   if (row < 0) return;
-  auto at = [&](int i) { return (2 * (size_t)(cta + i) + (i == 0 ? 1 : 0)) * N + n; };
+  auto at = [&](int i) { return (2 * (size_t)(cta + i * a.team) + (i == 0 ? 1 : 0)) * N + n; };
   float M = -INFINITY;
   for (int i = lane; i < parts; i += 32)
     if (a.part_l[at(i)] != 0.f) M = fmaxf(M, a.part_m[at(i)]);
@@ -853,6 +981,17 @@ int paged_rows(const PagedLaunch& L) {
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
 }
 
+// Key heads (or pairs) whose CTAs form a team: a divisor of them, up to FA_PAGED_TEAM.
+#ifndef FA_PAGED_TEAM
+#define FA_PAGED_TEAM 4
+#endif
+int team_size(int groups, int ctas) {
+  int best = 1;
+  for (int t = 2; t <= std::min({groups, ctas, FA_PAGED_TEAM}); ++t)
+    if (groups % t == 0 && ctas / t * t >= ctas / best * best * 31 / 32) best = t;
+  return best;
+}
+
 template <int N, bool kQ8, int D>
 fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
   using L = PagedLayout<N, kQ8>;
@@ -863,16 +1002,11 @@ fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
       }))
     return FA_ERR_CUDA;
   PagedArgs a;
-  int box = 128;
-  while (L0.page_size % box) box /= 2;
-  CUtensorMap tk, tv;
-  const long long rows = (long long)L0.num_pages * L0.page_size;
-  if (!encode_matrix_map(&tk, L0.k_pages, rows, L0.Hkv * D, kQ8, box) ||
-      !encode_matrix_map(&tv, L0.v_pages, rows, L0.Hkv * D, kQ8, box))
-    return FA_ERR_CUDA;
   const int ctas = num_sms();
   const PagedCarve c = paged_carve(ctas, N);
   uint8_t* ws = static_cast<uint8_t*>(L0.workspace);
+  a.k_pages = static_cast<const uint8_t*>(L0.k_pages);
+  a.v_pages = static_cast<const uint8_t*>(L0.v_pages);
   a.q = static_cast<const __nv_bfloat16*>(L0.q);
   a.q_stride = L0.q_stride;
   a.o = static_cast<__nv_bfloat16*>(L0.o);
@@ -889,14 +1023,19 @@ fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
   a.Hq = L0.Hq;
   a.Hkv = L0.Hkv;
   a.G = L0.Hq / L0.Hkv;
-  a.groups = D == 64 ? (L0.Hkv + 1) / 2 : L0.Hkv;
+  const int groups = D == 64 ? (L0.Hkv + 1) / 2 : L0.Hkv;
+  a.team = team_size(groups, ctas);
+  a.teams = ctas / a.team;
+  a.sets = groups / a.team;
   a.total_q = L0.total_q;
   a.max_q = L0.max_q;
   a.max_k = L0.max_k;
   a.num_pages = L0.num_pages;
   a.page_size = L0.page_size;
+  a.page_shift = 0;
+  while ((1LL << a.page_shift) < L0.page_size) ++a.page_shift;
+  a.page_mul = (uint32_t)((((1ull << a.page_shift) - (unsigned)L0.page_size) << 32) / (unsigned)L0.page_size + 1);
   a.max_pages = L0.max_pages;
-  a.box_rows = box;
   a.causal = L0.causal;
   a.scale_log2 = L0.scale * 1.4426950408889634f;
   a.meta = reinterpret_cast<int4*>(ws + c.meta);
@@ -907,12 +1046,13 @@ fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
   a.part_o = reinterpret_cast<float*>(ws + c.o);
   a.timeout_ns = L0.timeout_ns;
   prof_before(stream, kKPaged);
-  paged_kernel<N, kQ8, D><<<ctas, kThreads, L::kSmemBytes, stream>>>(tk, tv, a);
+  paged_kernel<N, kQ8, D><<<a.teams * a.team, kThreads, L::kSmemBytes, stream>>>(a);
   cudaError_t err = cudaGetLastError();
   prof_after(stream, kKPaged);
   if (err != cudaSuccess) return FA_ERR_CUDA;
+  if (L0.max_k <= kTile) return FA_OK;  // units of one tile are never split
   prof_before(stream, kKPagedMerge);
-  paged_merge_kernel<N, D><<<dim3(ctas, N / 4), 128, 0, stream>>>(a);
+  paged_merge_kernel<N, D><<<dim3(a.teams * a.team, N / 4), 128, 0, stream>>>(a);
   err = cudaGetLastError();
   prof_after(stream, kKPagedMerge);
   return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;

@@ -197,6 +197,25 @@ __device__ __forceinline__ void bulk_load_hint(void* dst, const void* src, uint3
       : "memory");
 }
 
+// 16 bytes global -> shared without passing registers, zeros instead when `have` is false
+// (src is then not read).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+
+// The first `bytes` (0 to 4) of a word global -> shared, zeros for the rest of it.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// One arrival on `bar` (counted at its initialisation) once this thread's cp.async copies
+// so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ----------------------------------------------------------------------------- register split
 
 // Executed by all four warps of a warpgroup: give registers back / take more.
@@ -338,6 +357,26 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&y)[N]) {
   for (int i = 0; i < N; ++i) y[i] = __uint_as_float(r[i / 16][i % 16]);
 }
 
+// N columns each at two places, loaded together and waited for once.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols2(uint32_t taddr_x, uint32_t taddr_y, float (&x)[N], float (&y)[N]) {
+  static_assert(N % 16 == 0, "whole groups of 16 columns");
+  uint32_t r[N / 8][16];
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i) {
+    tmem_ld16(taddr_x + 16 * i, r[2 * i]);
+    tmem_ld16(taddr_y + 16 * i, r[2 * i + 1]);
+  }
+  tmem_ld_wait16(r[0]);
+#pragma unroll
+  for (int i = 1; i < N / 8; ++i) reg_pin16(r[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = __uint_as_float(r[2 * (i / 16)][i % 16]);
+    y[i] = __uint_as_float(r[2 * (i / 16) + 1][i % 16]);
+  }
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -373,6 +412,13 @@ struct SDesc {
 
 __device__ __forceinline__ SDesc sdesc_make(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   const uint64_t d = sdesc_sw128(saddr, lbo, sbo);
+  return SDesc{static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)};
+}
+
+// MN-major operand without swizzle: groups of 16 bytes along M/N, `sbo` bytes apart; in a
+// group 16 bytes per K index, 8 of them (128 bytes) together, such eights `lbo` bytes apart.
+__device__ __forceinline__ SDesc sdesc_make_mn_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  const uint64_t d = sdesc_sw128(saddr, lbo, sbo) & ~(7ull << 61);
   return SDesc{static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)};
 }
 
@@ -533,12 +579,10 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                : "memory");
 }
 
-__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t x) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
-}
-
-__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t x) {
-  asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.b16 [%0], h;\n\t}" ::"r"(addr), "r"(x) : "memory");
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t x;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+  return x;
 }
 
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {

@@ -335,7 +335,8 @@ FA_API fa_status fa_decode_paged(const void* q, const void* k_pages, const void*
  *                      largest magnitude among the row's finite values, and rounds
  *                      x * 2^-e to the nearest e4m3 value (ties to even; magnitudes over
  *                      448 to 448; infinities and NaN to NaN).  Every stored value is a
- *                      bf16 number exactly.  Scale bytes outside [67, 187] are not checked
+ *                      bf16 number exactly.  The attention calls want both scale arrays
+ *                      4-byte aligned; scale bytes outside [67, 187] are not checked
  *                      and may overflow fp32 inside the attention calls.
  *   block_table      : device int32 [B, max_pages_per_seq]; entries past a sequence's
  *                      last page are not read

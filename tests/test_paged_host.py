@@ -56,7 +56,8 @@ def test_read_refusals(lib, kw, status):
 ATTEND = PAGES + [
     (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(lse=None), INVALID), (dict(lens=None), INVALID),
     (dict(Hq=6), INVALID), (dict(Hq=0), INVALID), (dict(maxk=65), INVALID), (dict(maxk=-1), INVALID),
-    (dict(q=P + 8), ALIGNMENT), (dict(o=P + 8), ALIGNMENT), (dict(lse=P + 4), ALIGNMENT), (dict(lens=P + 2), ALIGNMENT)]
+    (dict(q=P + 8), ALIGNMENT), (dict(o=P + 8), ALIGNMENT), (dict(lse=P + 4), ALIGNMENT), (dict(lens=P + 2), ALIGNMENT),
+    (dict(ks=P + 2), ALIGNMENT), (dict(vs=P + 1), ALIGNMENT)]
 
 
 @pytest.mark.parametrize("kw,status", ATTEND + [
