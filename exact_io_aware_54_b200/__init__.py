@@ -184,14 +184,13 @@ def paged_workspace(device=None, nbytes: int = 0) -> torch.Tensor:
     memory, so that graphs share it neither with each other nor with eager calls."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     global _paged_bytes
-    if not _paged_bytes:  # one call of few rows: what most calls need
-        _paged_bytes = fa_paged_workspace_size(1, 1, 1, 1, 1, 128)
-    nbytes = max(int(nbytes), _paged_bytes)
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
         ws[:256].zero_()  # the status word; the rest is written before it is read
         return ws
-    return workspace(nbytes, dev, f"paged:{_stream_ptr(dev)}")
+    if not _paged_bytes:  # what the largest call needs, so that it never has to grow
+        _paged_bytes = fa_paged_workspace_size(1, 64, 1, 4096, 4096, 128)
+    return workspace(max(int(nbytes), _paged_bytes), dev, f"paged:{_stream_ptr(dev)}")
 
 
 def _stream_ptr(device) -> int:

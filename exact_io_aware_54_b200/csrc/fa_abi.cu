@@ -20,7 +20,8 @@ namespace {
 const char* const kKernelNames[kKCount] = {"fa_fwd_kernel", "fa_bwd_preprocess_kernel", "fa_bwd_main_kernel",
                                            "fa_bwd_convert_kernel", "fa_decode_kernel",
                                            "fa_decode_check_kernel", "fa_cache_write_kernel",
-                                           "fa_cache_read_kernel", "fa_paged_kernel", "fa_paged_merge_kernel"};
+                                           "fa_cache_read_kernel", "fa_paged_kernel", "fa_paged_merge_kernel",
+                                           "fa_paged_chunk_kernel", "fa_paged_chunk_merge_kernel"};
 struct ProfRecord {
   int kernel;
   cudaEvent_t start, stop;
@@ -696,9 +697,18 @@ static bool paged_sizes_ok(int B, int Hq, int Hkv, int max_seqlen_q, int max_seq
          (rows / 32 + 1) * Hkv < (1LL << 31) / ((long long)max_seqlen_k / 128 + 1) && Hq < (1 << 16);
 }
 
+// Rows per key head up to which a sequence goes to the few-row kernel.
+#ifndef FA_PAGED_FEW_ROWS
+#define FA_PAGED_FEW_ROWS 16
+#endif
+static int paged_few_rows(int d) { return d == 64 ? FA_PAGED_FEW_ROWS / 2 : FA_PAGED_FEW_ROWS; }
+
 size_t fa_paged_workspace_size(int B, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int d) {
   if (!paged_sizes_ok(B, Hq, Hkv, max_seqlen_q, max_seqlen_k) || (d != 64 && d != 128)) return 0;
-  return paged_workspace_bytes();
+  // both kernels' states in the same place: they run one after the other
+  const size_t few = paged_few_workspace(FA_PAGED_FEW_ROWS);
+  if ((long long)max_seqlen_q * (Hq / Hkv) <= paged_few_rows(d)) return few;
+  return std::max(few, paged_chunk_workspace(d));
 }
 
 static fa_status fwd_paged(const void* q, long long q_row_stride, const void* k_pages, const void* v_pages,
@@ -721,7 +731,7 @@ static fa_status fwd_paged(const void* q, long long q_row_stride, const void* k_
   if (!aligned16(q) || q_row_stride % 8 || !aligned16(o) || !aligned16(lse) ||
       (reinterpret_cast<uintptr_t>(cu_seqlens_q) & 3u) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u))
     return FA_ERR_ALIGNMENT;
-  if (!workspace || !aligned16(workspace) || workspace_bytes < paged_workspace_bytes()) return FA_ERR_WORKSPACE;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < fa_paged_workspace_size(B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d)) return FA_ERR_WORKSPACE;
   PagedLaunch a;
   a.q = q;
   a.q_stride = q_row_stride;
@@ -751,7 +761,16 @@ static fa_status fwd_paged(const void* q, long long q_row_stride, const void* k_
   a.scale = resolve_scale(softmax_scale, d);
   a.workspace = workspace;
   a.timeout_ns = wait_timeout_ns();
-  return launch_paged(a, stream);
+  a.few_rows = paged_few_rows(d);
+  // A batch of short and long chunks: each kernel takes its own sequences (the lengths are
+  // on the device) and passes over the others.
+  const bool some_many = (long long)max_seqlen_q * (Hq / Hkv) > a.few_rows;
+  if (some_many && B == 1) a.few_rows = 0;  // one sequence: one launch, whatever its length
+  if (a.few_rows > 0) {
+    const fa_status s = launch_paged_few(a, stream);
+    if (s != FA_OK || !some_many) return s;
+  }
+  return launch_paged_chunk(a, stream);
 }
 
 fa_status fa_fwd_paged(const void* q, long long q_row_stride, const void* k_pages, const void* v_pages,

@@ -46,7 +46,8 @@ constexpr int kStatusBadArg = 1;
 
 // Kernels the library launches (for the optional launch profiler).
 enum KernelId { kKFwd = 0, kKBwdPre, kKBwdMain, kKBwdConvert, kKDecode, kKDecodeCheck, kKCacheWrite,
-                kKCacheRead, kKPaged, kKPagedMerge, kKCount };
+                kKCacheRead, kKPaged, kKPagedMerge, kKPagedChunk, kKPagedChunkMerge,
+                kKCount };
 // Bracket a launch with profiling events when profiling is on (no-ops otherwise).
 void prof_before(cudaStream_t s, int kernel_id);
 void prof_after(cudaStream_t s, int kernel_id);
@@ -240,12 +241,16 @@ struct PagedLaunch {
   float* lse;
   long long lse_head, lse_row;  // strides of lse over heads and tokens
   int B, Hq, Hkv, total_q, max_q, max_k, d, num_pages, page_size, max_pages, causal;
+  int few_rows;  // rows (new tokens x Hq / Hkv) up to which a sequence goes to the few-row kernel
   float scale;
   void* workspace;
   unsigned long long timeout_ns;
 };
-fa_status launch_paged(const PagedLaunch& a, cudaStream_t stream);
-size_t paged_workspace_bytes();
+fa_status launch_paged_few(const PagedLaunch& a, cudaStream_t stream);
+size_t paged_few_workspace(int rows);
+// The same for sequences of many rows (paged_chunk_sm100.cu).
+fa_status launch_paged_chunk(const PagedLaunch& a, cudaStream_t stream);
+size_t paged_chunk_workspace(int d);
 
 size_t decode_workspace_bytes(int B, int H, int d, const DecodePlan& plan);
 

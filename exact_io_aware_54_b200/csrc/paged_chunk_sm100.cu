@@ -1,0 +1,755 @@
+// paged_chunk_sm100.cu -- attention of many new rows per sequence over a paged key/value
+// cache in bf16 or 8 bits (B200, sm_100a): a prompt, or a later piece of one.
+//
+// The computation is that of paged_sm100.cu.  A unit is (sequence, key head, 256 rows), a
+// row being (token, query head of the key head's group): G query heads share every key
+// tile that is loaded, and a piece of 64 tokens with G = 4 fills a unit.  With this many
+// rows per key the tensor cores and the exponentials are the floor, as in the dense
+// forward, whose inner loop this is (fwd_sm100.cu, d = 128: scores and weights in tensor
+// memory, two 128-row tiles that take turns, P V in two halves, lazy rescale).  What differs:
+//
+//  * Rows.  The softmax threads load their own row of Q (any token stride, any G) into the
+//    swizzled tile and store their own row of O; a row's limit follows from its token.
+//  * Keys.  Pages are looked up by the warp of paged_common.cuh; four loader warps fill
+//    the K and V tiles, each 32 keys of every tile.  bf16: 16-byte asynchronous copies.
+//    8 bit: each lane loads 16 codes, multiplies by the row's scale and stores 16 bf16
+//    values.  A code times its power of two is a bf16 number, so the scores and products
+//    are those of the bf16 kernel on the dequantised cache, bit for bit, and the softmax
+//    warps, which bound the kernel, have nothing to add.
+//  * Work split: the line of all units' tiles, causal ones counted, is cut into equal
+//    parts, one per CTA (one CTA per SM).  A unit cut by a border leaves fp32 partial
+//    states of its 256 rows, two at most per CTA, which a second kernel joins in order.
+//    512 tokens over 16K keys (8 key heads, G = 4) are 64 units for 148 CTAs.
+//  * Warp roles (512 threads): 0 MMA issuer, 1 page lookup, 4-7 loaders, 8-11 and 12-15
+//    the softmax groups of the two row tiles; setmaxnreg 56 / 72 / 192 / 192.
+#include "paged_common.cuh"
+
+namespace fa {
+
+using namespace paged;
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr uint32_t kRegsIssue = 56, kRegsLoad = 72, kRegsSoftmax = 192;
+static_assert(kRegsIssue + kRegsLoad + 2 * kRegsSoftmax <= 4 * 128, "register split exceeds the launch budget");
+constexpr uint32_t kTmemCols = 512;
+constexpr int kUnitRows = 256;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+__host__ __device__ constexpr uint32_t tm_s(int t) { return t * 128u; }
+template <int D>
+__host__ __device__ constexpr uint32_t tm_o(int t) {
+  return 256u + t * (uint32_t)D;
+}
+
+template <int D>
+struct ChunkLayout {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kBoxBytes = 128 * 128;  // a 64-column (128-byte) block of a tile's rows
+  static constexpr int kStages = D == 64 ? 8 : 4;
+  static constexpr int kRing = 8;               // tiles that the page lookup may be ahead
+  static constexpr int kOffSlots = 2 * kTileBytes;  // behind the two Q tiles
+  static constexpr int kOffScales = kOffSlots + kStages * kTileBytes;
+  static constexpr int kOffRows = kOffScales + kRing * kTile * 16;
+  static constexpr int kOffTile = kOffRows + kRing * kTile * 4;
+  static constexpr int kOffBar = kOffTile + kRing * 4;
+  // kv_full[S], kv_empty[S], rows_full[R], rows_empty[R], q_full[2], s_full[2], p_half[2], p_full[2], o_done[2]
+  static constexpr int kNumBars = 2 * kStages + 2 * kRing + 10;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffWalk = (kOffMisc + 80 + 15) & ~15;
+  static constexpr int kSmemBytes = kOffWalk + 8 * 160 + 1024;  // + alignment slack
+  static_assert(kSmemBytes <= 232448, "shared memory of one SM");
+};
+
+struct Work {
+  long long pos, end, total;
+  int b, off;
+  int ctas;
+};
+
+// Keys that rows up to `row` of a unit's sequence see, and the tiles of them (one, fully
+// masked, when there are none).
+__device__ __forceinline__ int keys_of(const PagedArgs& a, const SeqInfo& s, int row) {
+  if (!a.causal) return s.lk;
+  const int token = min(row / a.G, s.nq - 1);
+  return max(0, min(s.lk, s.lk - s.nq + token + 1));
+}
+__device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kTile - 1) / kTile); }
+__device__ __forceinline__ int units_of(const PagedArgs& a, int nq) {
+  return nq <= 0 ? 0 : (nq * a.G + kUnitRows - 1) / kUnitRows;
+}
+// Tiles of unit u of a key head.
+__device__ __forceinline__ int unit_tiles(const PagedArgs& a, const SeqInfo& s, int u) {
+  return tiles_of(keys_of(a, s, u * kUnitRows + kUnitRows - 1));
+}
+// Tiles of one key head of a sequence: all its units'.
+__device__ __forceinline__ int head_tiles(const PagedArgs& a, const SeqInfo& s) {
+  const int units = units_of(a, s.nq);
+  if (!a.causal) return units * tiles_of(s.lk);
+  int n = 0;
+  for (int u = 0; u < units; ++u) n += unit_tiles(a, s, u);
+  return n;
+}
+
+struct Piece {
+  int b, hk, unit, t0, t1, tiles;
+  SeqInfo s;
+};
+// The sequences' head_tiles are only recomputed when the stretch enters a sequence
+// (w.off < 0: not yet).
+struct Walk {
+  Work w;
+  SeqInfo s;
+  int hk, unit, t;  // where pos is
+  bool inside;
+};
+__device__ __forceinline__ void enter(const PagedArgs& a, Walk& k) {
+  // from w.off tiles into sequence w.b
+  k.s = seq_info(a, k.w.b);
+  const int per_head = head_tiles(a, k.s);
+  k.hk = per_head ? k.w.off / per_head : 0;
+  int rest = k.w.off - k.hk * per_head;
+  k.unit = 0;
+  const int units = units_of(a, k.s.nq);
+  while (k.unit < units) {
+    const int n = unit_tiles(a, k.s, k.unit);
+    if (rest < n) break;
+    rest -= n;
+    ++k.unit;
+  }
+  k.t = rest;
+  k.inside = true;
+}
+__device__ __forceinline__ bool next_piece(const PagedArgs& a, Walk& k, Piece& p) {
+  if (k.w.pos >= k.w.end) return false;
+  if (!k.inside) enter(a, k);
+  while (k.hk >= a.Hkv || units_of(a, k.s.nq) == 0) {  // past the sequence's last head: the next sequence with rows
+    if (++k.w.b >= a.B) return false;
+    k.s = seq_info(a, k.w.b);
+    k.hk = k.unit = k.t = 0;
+  }
+  p.s = k.s;
+  p.b = k.w.b;
+  p.hk = k.hk;
+  p.unit = k.unit;
+  p.tiles = unit_tiles(a, k.s, k.unit);
+  p.t0 = k.t;
+  p.t1 = (int)min((long long)p.tiles, k.t + (k.w.end - k.w.pos));
+  k.w.pos += p.t1 - p.t0;
+  k.t = p.t1;
+  if (k.t == p.tiles) {
+    k.t = 0;
+    if (++k.unit == units_of(a, k.s.nq)) {
+      k.unit = 0;
+      ++k.hk;
+    }
+  }
+  return true;
+}
+
+// Run by one warp: the line's length and where this CTA's stretch begins.
+__device__ __forceinline__ Work find_work(const PagedArgs& a) {
+  const int lane = lane_id();
+  Work w;
+  auto cost_of = [&](int b) {
+    if (b >= a.B) return 0;
+    const SeqInfo s = seq_info(a, b);
+    if (s.nq < 0 && blockIdx.x == 0) atomicExch(a.status, kStatusBadArg);
+    return s.nq > 0 ? head_tiles(a, s) * a.Hkv : 0;
+  };
+  long long total = 0;
+  for (int b = lane; b < a.B; b += 32) total += cost_of(b);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  w.total = total;
+  w.ctas = (int)min((long long)gridDim.x, total);
+  w.b = 0;
+  w.off = 0;
+  w.pos = w.end = 0;
+  if ((int)blockIdx.x >= w.ctas) return w;
+  w.pos = total * blockIdx.x / w.ctas;
+  w.end = total * (blockIdx.x + 1) / w.ctas;
+  long long before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int mine = cost_of(b0 + lane);
+    long long upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += x;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + upto > w.pos);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      w.b = b0 + src;
+      w.off = (int)(w.pos - (before + __shfl_sync(0xffffffffu, upto - mine, src)));
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return w;
+}
+
+// S = Q K^T, 128 x 128: as in the dense forward.
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, SDesc q, SDesc k) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;  // 16-byte units
+    umma_ss(d_tmem, sdesc_at(q, off), sdesc_at(k, off), idesc, kk > 0 ? 1u : 0u);
+  }
+}
+// O (+)= P V for keys 64 half .. 64 half + 63, P bf16 in tensor memory.
+template <int D>
+__device__ __forceinline__ void issue_pv_half(uint32_t o_tmem, uint32_t p_tmem, SDesc v, bool accumulate, int half) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, D, false, true);
+#pragma unroll
+  for (int k4 = 0; k4 < 4; ++k4) {
+    const int kk = 4 * half + k4;
+    umma_ts(o_tmem, p_tmem + kk * 8, sdesc_at(v, kk * 128), idesc, (accumulate || kk > 0) ? 1u : 0u);
+  }
+}
+
+// Four e4m3 codes times f, as bf16 (exact).
+__device__ __forceinline__ uint2 scaled_codes(uint32_t q, float f) {
+  const float2 x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q & 0xFFFFu), __NV_E4M3)));
+  const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q >> 16), __NV_E4M3)));
+  const float2 f2 = make_float2(f, f);
+  const float2 xs = fmul2(x, f2), ys = fmul2(y, f2);
+  return make_uint2(pack_bf16x2(xs.x, xs.y), pack_bf16x2(ys.x, ys.y));
+}
+
+template <int D, bool kQ8>
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArgs a) {
+  using L = ChunkLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* kv_empty = kv_full + L::kStages;
+  uint64_t* rows_full = kv_empty + L::kStages;
+  uint64_t* rows_empty = rows_full + L::kRing;
+  uint64_t* q_full = rows_empty + L::kRing;
+  uint64_t* s_full = q_full + 2;
+  uint64_t* p_half = q_full + 4;
+  uint64_t* p_full = q_full + 6;
+  uint64_t* o_done = q_full + 8;
+  uint32_t* ring_rows = reinterpret_cast<uint32_t*>(smem + L::kOffRows);
+  volatile int* ring_tile = reinterpret_cast<volatile int*>(smem + L::kOffTile);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+  Work* work = reinterpret_cast<Work*>(smem + (L::kOffMisc + 15) / 8 * 8);
+  const uint32_t warp = warp_id(), lane = lane_id();
+
+  if (warp == 8) {
+    const Work w = find_work(a);
+    if (lane == 0) {
+      *work = w;
+      a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(kv_full + s, kQ8 ? 4 : 128);  // a loader warp, or each copying lane
+      mbar_init(kv_empty + s, 1);
+    }
+    for (int i = 0; i < L::kRing; ++i) {
+      mbar_init(rows_full + i, kQ8 ? 33 : 1);
+      mbar_init(rows_empty + i, 4);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full + t, 4);
+      mbar_init(s_full + t, 1);
+      mbar_init(p_half + t, 4);
+      mbar_init(p_full + t, 4);
+      mbar_init(o_done + t, 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk walk;
+  walk.w = *work;
+  walk.inside = false;
+  auto give_up = [&]() {
+    *abort_flag = 1;
+    atomicCAS(a.status, 0, kStatusTimeout);
+  };
+
+  if (warp < 4) {
+    regs_dec<kRegsIssue>();
+    if (warp == 1) {
+      // ------------------------------------------------------------------ page lookup
+      const PageRing ring{ring_rows, ring_tile, smem_u32(smem + L::kOffScales), rows_full, rows_empty};
+      const bool ok = look_up_pages<L::kRing, kQ8, false>(a, ring, abort_flag, [&](int& b, int& hk, int& t0, int& t1, int& lk) {
+        Piece p;
+        if (!next_piece(a, walk, p)) return false;
+        b = p.b, hk = p.hk, t0 = p.t0, t1 = p.t1, lk = p.s.lk;
+        return true;
+      });
+      if (!ok && lane == 0) give_up();
+    } else if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------------ MMA issuer
+      const uint32_t base = smem_u32(smem);
+      const SDesc q_desc[2] = {sdesc_make(base, 16, 1024), sdesc_make(base + L::kTileBytes, 16, 1024)};
+      const SDesc ring_k = sdesc_make(base + L::kOffSlots, 16, 1024);            // K tiles, K-major
+      const SDesc ring_v = sdesc_make(base + L::kOffSlots, L::kBoxBytes, 1024);  // V tiles, MN-major
+      constexpr uint32_t kSlot16 = L::kTileBytes / 16;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !thread_wait(bar, parity, a.timeout_ns, abort_flag)) {
+          give_up();
+          ok = false;
+        }
+        return ok;
+      };
+      uint32_t g = 0, q_cnt[2] = {0, 0}, p_cnt[2] = {0, 0};
+      auto slot_ready = [&](uint32_t i) {
+        if (!wait(kv_full + i % L::kStages, (i / L::kStages) & 1)) return false;
+        fence_proxy_async_smem();  // the loaders' writes, before the tensor core reads them
+        tc_fence_after();
+        return true;
+      };
+      Piece p;
+      while (ok && next_piece(a, walk, p)) {
+        // tiles of the unit that each row tile needs; the second may have no row
+        const int rows = p.s.nq * a.G - p.unit * kUnitRows;
+        const int nt[2] = {min(p.t1, tiles_of(keys_of(a, p.s, p.unit * kUnitRows + 127))), rows > 128 ? p.t1 : p.t0};
+        bool have[2] = {p.t0 < nt[0], p.t0 < nt[1]};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (t == 0 || rows > 128) {
+            if (!wait(q_full + t, q_cnt[t]++ & 1)) break;
+          }
+        if (!ok) break;
+        tc_fence_after();
+        if (!slot_ready(g)) break;
+        {
+          const SDesc k = SDesc{ring_k.lo + (g % L::kStages) * kSlot16, ring_k.hi};
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (have[t]) {
+              issue_qk<D>(tmem + tm_s(t), q_desc[t], k);
+              umma_commit(s_full + t);
+            }
+          umma_commit(kv_empty + g % L::kStages);
+          ++g;
+        }
+        for (int j = p.t0; j < p.t1 && ok; ++j) {
+          const uint32_t gv = g++, slot_v = gv % L::kStages;
+          if (!slot_ready(gv)) break;
+          const SDesc v = SDesc{ring_v.lo + slot_v * kSlot16, ring_v.hi};
+          const bool more = j + 1 < p.t1;
+          SDesc k = ring_k;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (j < nt[t]) {
+              if (!wait(p_half + t, p_cnt[t] & 1)) break;
+              tc_fence_after();
+              issue_pv_half<D>(tmem + tm_o<D>(t), tmem + tm_s(t), v, j > p.t0, 0);
+              if (!wait(p_full + t, p_cnt[t] & 1)) break;
+              tc_fence_after();
+              ++p_cnt[t];
+              issue_pv_half<D>(tmem + tm_o<D>(t), tmem + tm_s(t), v, true, 1);
+            }
+            if (t == 0 && more) {
+              if (!slot_ready(g)) break;
+              k = SDesc{ring_k.lo + (g % L::kStages) * kSlot16, ring_k.hi};
+            }
+            if (more && j + 1 < nt[t]) {
+              issue_qk<D>(tmem + tm_s(t), q_desc[t], k);
+              umma_commit(s_full + t);
+            }
+          }
+          if (!ok) break;
+          umma_commit(kv_empty + slot_v);
+          if (more) {
+            umma_commit(kv_empty + g % L::kStages);
+            ++g;
+          }
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (t == 0 || rows > 128) umma_commit(o_done + t);
+      }
+    }
+  } else if (warp < 8) {
+    regs_dec<kRegsLoad>();
+    // ------------------------------------------------------------------ loaders: keys 32 (warp - 4) .. of every tile
+    constexpr int kChunks = D * (kQ8 ? 1 : 2) / 16;  // 16-byte pieces of a cache row's slice
+    constexpr int kKeys = 32 / kChunks;              // keys per step of the warp
+    constexpr int kSteps = 32 / kKeys;
+    const uint32_t row_bytes = (uint32_t)a.Hkv * D * (kQ8 ? 1 : 2);
+    const int chunk = lane % kChunks, sub = lane / kChunks, first = (warp - 4) * 32;
+    const uint32_t ring = smem_u32(ring_rows), words = smem_u32(smem + L::kOffScales);
+    bool ok = true;
+    for (uint32_t c = 0; ok; ++c) {
+      const uint32_t at = c % L::kRing;
+      ok = warp_wait(rows_full + at, (c / L::kRing) & 1, a.timeout_ns, abort_flag);
+      if (!ok) break;
+      const int hk = ring_tile[at];
+      if (hk < 0) break;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t g = 2 * c + kv, slot = g % L::kStages;
+        const uint8_t* src = (kv ? a.v_pages : a.k_pages) + (size_t)hk * D * (kQ8 ? 1 : 2) + chunk * 16;
+        const uint32_t tile = smem_u32(smem + L::kOffSlots + slot * L::kTileBytes);
+        uint32_t rw[kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) rw[i] = ld_shared_u32(ring + (at * kTile + first + i * kKeys + sub) * 4);
+        if constexpr (kQ8) {
+          uint4 q[kSteps];
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+            q[i] = rw[i] != kNoRow ? __ldg(reinterpret_cast<const uint4*>(src + (uint64_t)rw[i] * row_bytes)) : make_uint4(0, 0, 0, 0);
+          ok = warp_wait(kv_empty + slot, ((g / L::kStages) & 1) ^ 1, a.timeout_ns, abort_flag);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const int key = first + i * kKeys + sub;
+            const uint32_t word = ld_shared_u32(words + (at * kTile + key) * 16 + kv * 8);
+            const uint32_t cut = ((rw[i] * (uint32_t)a.Hkv + hk) & 3u) * 8;
+            const float f = rw[i] != kNoRow ? __uint_as_float(((word >> cut) & 0xFFu) << 23) : 0.f;
+            const uint2 w0 = scaled_codes(q[i].x, f), w1 = scaled_codes(q[i].y, f), w2 = scaled_codes(q[i].z, f),
+                        w3 = scaled_codes(q[i].w, f);
+            const int c2 = 2 * chunk;  // 16-byte chunks of the bf16 row: c2 and c2 + 1
+            const uint32_t row = tile + (c2 >> 3) * L::kBoxBytes + key * 128;
+            st_shared_v4(row + (((c2 & 7) ^ (key & 7)) << 4), w0.x, w0.y, w1.x, w1.y);
+            st_shared_v4(row + ((((c2 & 7) + 1) ^ (key & 7)) << 4), w2.x, w2.y, w3.x, w3.y);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive_warp(kv_full + slot);
+        } else {
+          ok = warp_wait(kv_empty + slot, ((g / L::kStages) & 1) ^ 1, a.timeout_ns, abort_flag);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const int key = first + i * kKeys + sub;
+            const bool have = rw[i] != kNoRow;
+            cp_async16_or_zero(tile + (chunk >> 3) * L::kBoxBytes + key * 128 + (((chunk & 7) ^ (key & 7)) << 4),
+                               src + (uint64_t)(have ? rw[i] : 0u) * row_bytes, have);
+          }
+          cp_async_arrive(kv_full + slot);
+        }
+      }
+      mbar_arrive_warp(rows_empty + at);
+    }
+    if (!ok && lane == 0) give_up();
+    if constexpr (!kQ8) cp_async_wait_all();
+  } else {
+    regs_inc<kRegsSoftmax>();
+    // ------------------------------------------------------------------ softmax groups
+    const int t = (warp - 8) >> 2;
+    const uint32_t quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // row of the tile
+    const uint32_t lanes = (quarter * 32) << 16;
+    const uint32_t tS = tmem + lanes + tm_s(t), tO = tmem + lanes + tm_o<D>(t);
+    uint32_t s_cnt = 0, items = 0;
+    // the warp's place in the line lies in shared memory: registers are for the scores
+    struct Place {
+      Walk walk;
+      Piece p;
+    };
+    static_assert(sizeof(Place) <= 160, "the place fits");
+    Place* place = reinterpret_cast<Place*>(smem + L::kOffWalk + (warp - 8) * 160);
+    if (lane == 0) place->walk = walk;
+    for (;;) {
+      __syncwarp();
+      int more = 0;
+      if (lane == 0) {
+        Walk k = place->walk;
+        Piece q;
+        more = next_piece(a, k, q);
+        if (more) {
+          place->walk = k;
+          place->p = q;
+        }
+      }
+      if (__shfl_sync(0xffffffffu, more, 0) == 0) break;
+      __syncwarp();
+      const Piece& p = place->p;
+      const int row0 = p.unit * kUnitRows + t * 128;
+      const int rows = p.s.nq * a.G - row0;  // of this tile
+      if (rows <= 0) continue;               // (the second tile of a short unit)
+      const int row = row0 + r, token = row / a.G, head = p.hk * a.G + (row - token * a.G);
+      const bool mine = r < rows;
+      // Q: every MMA that read the tile has completed (o_done of the piece before)
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)(p.s.qoff + token) * a.q_stride + (long long)head * D);
+        const uint32_t dst = smem_u32(smem) + t * L::kTileBytes + r * 128;
+        uint4 x[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = mine ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          st_shared_v4(dst + (i >> 3) * L::kBoxBytes + (((i & 7) ^ (r & 7)) << 4), x[i].x, x[i].y, x[i].z, x[i].w);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive_warp(q_full + t);
+
+      const int lim = mine ? keys_of(a, p.s, row) : 0;
+      const int first_lim = keys_of(a, p.s, row0);  // the fewest keys that a row of the tile sees
+      const int nt = min(p.t1, tiles_of(keys_of(a, p.s, row0 + 127)));
+      float m2 = -INFINITY, l = 0.f, le = 0.f;
+      bool ok = true;
+#pragma unroll 1
+      for (int j = p.t0; j < nt; ++j) {
+        if (!warp_wait(s_full + t, s_cnt & 1, a.timeout_ns, abort_flag)) {
+          if (lane == 0) give_up();
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(tS + i * 32, s[i]);
+        tmem_ld_wait(s[0]);
+        reg_pin(s[1]);
+        reg_pin(s[2]);
+        reg_pin(s[3]);
+        const int kbase = j * kTile;
+        if (kbase + kTile > first_lim) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (kbase + i * 32 + c >= lim) s[i][c] = __float_as_uint(-INFINITY);
+        }
+        float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 32; c += 2)
+            mxv[i] = fmax3(mxv[i], __uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1]));
+        const float m_tile = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])) * a.scale_log2;
+        const bool need = (m2 == -INFINITY) || (m_tile > m2 + kRescaleThreshold);
+        const float m_use = need ? fmaxf(m2, m_tile) : m2;
+        const float alpha = (m2 == -INFINITY) ? 0.f : ex2(m2 - m_use);
+        const float m_ref = (m_use == -INFINITY) ? 0.f : m_use;
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(-m_ref, -m_ref);
+        float2 ex0 = make_float2(0.f, 0.f), ex1 = ex0, rd0 = ex0, rd1 = ex0;  // unrounded and bf16 sums
+        auto exp_half = [&](int hf, uint32_t(&pk)[32]) {
+#pragma unroll
+          for (int ii = 0; ii < 2; ++ii) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const uint32_t* sr = s[hf * 2 + ii];
+              const float2 x0 = ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, nm2);
+              const float2 x1 = ffma2(make_float2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sc2, nm2);
+              const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y));
+              // a sixteenth of the exponentials on the FMA pipes, as in the dense forward
+              const float2 p1 = ((c >> 2) % 8 == 7) ? exp2_fma2(x1) : make_float2(ex2(x1.x), ex2(x1.y));
+              const uint32_t k0 = pack_bf16x2(p0.x, p0.y), k1 = pack_bf16x2(p1.x, p1.y);
+              pk[ii * 16 + (c >> 1)] = k0;
+              pk[ii * 16 + (c >> 1) + 1] = k1;
+              ex0 = fadd2(ex0, p0);
+              ex1 = fadd2(ex1, p1);
+              acc_bf16x2(rd0, k0);
+              acc_bf16x2(rd1, k1);
+            }
+          }
+        };
+        // the previous P V of this tile has completed: the scores just read were issued
+        // after it, and tcgen05 operations complete in order
+        if (j > p.t0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld32(tO + cc * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tmem_st32(tO + cc * 32, o);
+          }
+        }
+        uint32_t pk[32];
+        exp_half(0, pk);
+        tmem_st32(tS, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(p_half + t);
+        exp_half(1, pk);
+        tmem_st32(tS + 32, pk);
+        l = l * alpha + ((rd0.x + rd0.y) + (rd1.x + rd1.y));
+        le = le * alpha + ((ex0.x + ex0.y) + (ex1.x + ex1.y));
+        m2 = m_use;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(p_full + t);
+        ++s_cnt;
+      }
+      if (!ok) break;
+      // ---- epilogue
+      if (!warp_wait(o_done + t, items & 1, a.timeout_ns, abort_flag)) {
+        if (lane == 0) give_up();
+        break;
+      }
+      ++items;
+      tc_fence_after();
+      const bool whole = p.t0 == 0 && p.t1 == p.tiles;
+      const int out_token = p.s.qoff + (p.unit * kUnitRows + t * 128 + r) / a.G;  // (worked out again rather than kept)
+      const int out_head = p.hk * a.G + (p.unit * kUnitRows + t * 128 + r) % a.G;
+      const int out_row = mine ? out_token * a.Hq + out_head : -1;
+      if (whole) {
+        const float inv = (l > 0.f) ? 1.f / l : (l == 0.f ? 0.f : l);
+        uint4* dst = reinterpret_cast<uint4*>(a.o + (size_t)max(out_row, 0) * D);
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(tO + cc * 32, o);
+          tmem_ld_wait(o);
+          if (mine) {
+            const bool none = l == 0.f;  // every key hidden: O = 0, whatever V holds
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              const float* f = reinterpret_cast<const float*>(o) + q4 * 8;
+              uint4 x = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                                   pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
+              if (none) x = make_uint4(0, 0, 0, 0);
+              dst[cc * 4 + q4] = x;
+            }
+          }
+        }
+        if (mine)
+          a.lse[out_token * a.lse_row + out_head * a.lse_head] =
+              le == 0.f ? -INFINITY : (m2 + __log2f(le)) * 0.69314718055994530942f;
+      } else {
+        // slot 0: goes on with a unit begun before; slot 1: a unit begun here.  O as
+        // [d / 4][128 rows] of float4, so that a warp's stores are contiguous
+        const size_t slot = 2 * (size_t)blockIdx.x + (p.t0 == 0 ? 1 : 0);
+        float4* dst = reinterpret_cast<float4*>(a.part_o) + (slot * 2 + t) * (D / 4) * 128 + r;
+        if (p.t0 < nt) {
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld32(tO + cc * 32, o);
+            tmem_ld_wait(o);
+            const float* f = reinterpret_cast<const float*>(o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[(cc * 8 + i) * 128] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+          }
+        }
+        const size_t at = slot * kUnitRows + t * 128 + r;
+        a.part_m[at] = m2;
+        a.part_l[at] = le;
+        a.part_lr[at] = l;
+        if (p.t0 == 0) {
+          a.part_rows[(size_t)blockIdx.x * kUnitRows + t * 128 + r] = out_row;
+          if (t == 0 && r == 0) {
+            const Work& w = place->walk.w;
+            const long long last = w.pos - p.t1 + p.tiles - 1;  // the unit's last tile
+            a.meta[blockIdx.x] =
+                make_int4((int)(((last + 1) * w.ctas - 1) / w.total) - (int)blockIdx.x + 1, rows > 128 ? 2 : 1, 0, 0);
+          }
+        }
+      }
+      tc_fence_before();  // O is read before the next piece's products overwrite it (q_full orders them)
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the partial states of the unit that begins in attention CTA blockIdx.x: 128 rows
+// (blockIdx.y of the unit), 32 dims (blockIdx.z), a thread per row.
+template <int D>
+__global__ void __launch_bounds__(128) paged_chunk_merge_kernel(const PagedArgs a) {
+  const int cta = blockIdx.x, t = blockIdx.y, r = threadIdx.x;
+  const int4 meta = a.meta[cta];
+  const int parts = meta.x;
+  if (parts == 0 || t >= meta.y) return;
+  const int row = a.part_rows[(size_t)cta * kUnitRows + t * 128 + r];
+  auto slot = [&](int i) { return 2 * (size_t)(cta + i) + (i == 0 ? 1 : 0); };
+  float M = -INFINITY;
+  for (int i = 0; i < parts; ++i) {
+    const size_t at = slot(i) * kUnitRows + t * 128 + r;
+    if (a.part_l[at] != 0.f) M = fmaxf(M, a.part_m[at]);
+  }
+  float acc[32], l = 0.f, lr = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const size_t at = slot(i) * kUnitRows + t * 128 + r;
+    const float pl = a.part_l[at];
+    if (pl == 0.f) continue;  // no key in this part: its O was not written
+    const float wt = ex2(a.part_m[at] - M);
+    l = fmaf(wt, pl, l);
+    lr = fmaf(wt, a.part_lr[at], lr);
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + (slot(i) * 2 + t) * (D / 4) * 128 + blockIdx.z * 8 * 128 + r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float4 x = src[e * 128];
+      acc[4 * e] = fmaf(wt, x.x, acc[4 * e]);
+      acc[4 * e + 1] = fmaf(wt, x.y, acc[4 * e + 1]);
+      acc[4 * e + 2] = fmaf(wt, x.z, acc[4 * e + 2]);
+      acc[4 * e + 3] = fmaf(wt, x.w, acc[4 * e + 3]);
+    }
+  }
+  if (row < 0) return;
+  const float inv = lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr);
+  uint4* dst = reinterpret_cast<uint4*>(a.o + (size_t)row * D + blockIdx.z * 32);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float* f = acc + 8 * i;
+    dst[i] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                        pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
+  }
+  if (blockIdx.z == 0) {
+    const int token = row / a.Hq, head = row - token * a.Hq;
+    a.lse[token * a.lse_row + head * a.lse_head] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.69314718055994530942f;
+  }
+}
+
+template <int D, bool kQ8>
+fa_status launch_chunk_impl(const PagedLaunch& L0, cudaStream_t stream) {
+  using L = ChunkLayout<D>;
+  static PerDeviceOnce attr_once;
+  if (!attr_once.run([] {
+        return cudaFuncSetAttribute(paged_chunk_kernel<D, kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    L::kSmemBytes) == cudaSuccess;
+      }))
+    return FA_ERR_CUDA;
+  const int ctas = num_sms();
+  PagedArgs a = paged_args(L0);
+  paged_carve(ctas, kUnitRows, D).place(a, L0.workspace);
+  a.min_rows = L0.few_rows + 1;
+  a.max_rows = 0x7fffffff;
+  prof_before(stream, kKPagedChunk);
+  paged_chunk_kernel<D, kQ8><<<ctas, kThreads, L::kSmemBytes, stream>>>(a);
+  cudaError_t err = cudaGetLastError();
+  prof_after(stream, kKPagedChunk);
+  if (err != cudaSuccess) return FA_ERR_CUDA;
+  if (L0.max_k <= kTile) return FA_OK;  // units of one tile are never split
+  prof_before(stream, kKPagedChunkMerge);
+  paged_chunk_merge_kernel<D><<<dim3(ctas, 2, D / 32), 128, 0, stream>>>(a);
+  err = cudaGetLastError();
+  prof_after(stream, kKPagedChunkMerge);
+  return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t paged_chunk_workspace(int d) { return paged_carve(num_sms(), kUnitRows, d).bytes; }
+
+fa_status launch_paged_chunk(const PagedLaunch& L, cudaStream_t stream) {
+  const bool q8 = L.k_scales != nullptr;
+  if (L.d == 64) return q8 ? launch_chunk_impl<64, true>(L, stream) : launch_chunk_impl<64, false>(L, stream);
+  return q8 ? launch_chunk_impl<128, true>(L, stream) : launch_chunk_impl<128, false>(L, stream);
+}
+
+}  // namespace fa

@@ -1,0 +1,258 @@
+// paged_common.cuh -- what the kernels of attention over a paged cache share: arguments,
+// sequences, and the warp that turns tiles of keys into rows of the cache.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "fa_internal.h"
+#include "ptx.cuh"
+
+namespace fa {
+
+namespace paged {
+
+constexpr int kTile = 128;  // keys per tile
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;  // past the sequence's end
+
+struct PagedArgs {
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const __nv_bfloat16* q;
+  long long q_stride;  // elements between tokens
+  __nv_bfloat16* o;
+  float* lse;
+  long long lse_head, lse_row;  // strides of lse
+  const int32_t* cu_q;          // null: one token per sequence
+  const int32_t* table;
+  const int32_t* seqlens;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  int* status;
+  int B, Hq, Hkv, G;
+  int team, teams, sets;  // CTAs (key heads, or pairs of them when d = 64) of a team, teams, teams' worths of heads
+  int total_q, max_q, max_k;
+  int num_pages, page_size, max_pages;
+  uint32_t page_mul, page_shift;  // division by page_size
+  long long scale_bytes;          // of k_scales, v_scales
+  // sequences of min_rows to max_rows rows (new tokens times G) are this kernel's
+  int min_rows, max_rows;
+  int causal;
+  float scale_log2;
+  // partial states, for N rows a unit
+  int4* meta;       // [CTAs]: parts of the unit that begins in this CTA and ends in a later one
+  int* part_rows;   // [CTAs, N] its rows' output rows (-1: none)
+  float* part_m;    // [2 CTAs, N] reference, log2 units
+  float* part_l;    // [2 CTAs, N] sum of the unrounded weights
+  float* part_lr;   // [2 CTAs, N] the sum that divides O
+  float* part_o;    // [2 CTAs, ...] O, N rows of 128 or d dims
+  unsigned long long timeout_ns;
+};
+
+// Bounded waits, false also when another role of the CTA has given up.  A phase that is
+// complete at the first look costs no more than that look (every lane's, so that nothing
+// has to be handed over).
+__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns,
+                                            volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, timeout_ns) && !*abort_flag;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns,
+                                          volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  bool ok = true;
+  if (lane_id() == 0) ok = mbar_wait(bar, parity, timeout_ns) && !*abort_flag;
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// Sequence b: new tokens, keys and first packed row; nq = -1 when its offsets do not fit,
+// 0 when it is not this kernel's.
+struct SeqInfo {
+  int nq, lk, qoff;
+};
+__device__ __forceinline__ SeqInfo seq_info(const PagedArgs& a, int b) {
+  SeqInfo s;
+  s.lk = max(0, min(a.seqlens[b], a.max_k));
+  if (a.cu_q == nullptr) {
+    s.nq = 1;
+    s.qoff = b;
+    return s;
+  }
+  s.qoff = a.cu_q[b];
+  const int end = a.cu_q[b + 1];
+  if (s.qoff < 0 || end < s.qoff || end > a.total_q) {
+    s.nq = -1;
+    return s;
+  }
+  s.nq = min(end - s.qoff, a.max_q);
+  if (s.nq * a.G < a.min_rows || s.nq * a.G > a.max_rows) s.nq = 0;  // another kernel's
+  return s;
+}
+
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, "Division by
+// Invariant Integers using Multiplication", 1994): s = ceil(log2 d), m = floor(2^32 (2^s - d)
+// / d) + 1, n / d = (hi(m n) + n) >> s.
+__device__ __forceinline__ int page_index(const PagedArgs& a, int n) {
+  return (int)((__umulhi(a.page_mul, (uint32_t)n) + (uint32_t)n) >> a.page_shift);
+}
+
+__device__ __forceinline__ float redux_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+
+// A ring of tiles in shared memory, written by the lookup warp: the rows of the flattened
+// pages that hold the tile's keys (kNoRow past the sequence's end), the key head (or pair of
+// heads), -1 after the last tile, and in 8 bits per key the words that hold its K and V
+// scale bytes, two each when the heads of a pair may lie in different words.  `full` counts
+// one arrival, in 8 bits 33; the readers arrive on `empty`.
+struct PageRing {
+  uint32_t* rows;
+  volatile int* tile;
+  uint32_t scales;  // shared-memory address, 16 bytes per key
+  uint64_t* full;
+  uint64_t* empty;
+};
+
+// Run by one warp.  next(b, head, t0, t1, lk): the next stretch of tiles, false at the end.
+// A page outside the cache is recorded and read as page 0.  The pages of a tile are loaded
+// while the one before is written out.  Returns false when a wait gave up.
+template <int kRing, bool kQ8, bool kPair, class Next>
+__device__ __forceinline__ bool look_up_pages(const PagedArgs& a, const PageRing& ring, volatile int* abort_flag, Next next) {
+  const int lane = lane_id();
+  uint32_t c = 0;
+  bool ok = true;
+  auto publish = [&](const int(&page)[4], int key0, int lk, int head) {
+    const uint32_t at = c % kRing;
+    ok = warp_wait(ring.empty + at, ((c / kRing) & 1) ^ 1, a.timeout_ns, abort_flag);
+    if (!ok) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = key0 + lane + 32 * i;
+      int pg = page[i];
+      if (pg < 0 || pg >= a.num_pages) {  // never read outside the cache
+        atomicExch(a.status, kStatusBadArg);
+        pg = 0;
+      }
+      const uint32_t row = (uint32_t)(pg * a.page_size + (key - page_index(a, key) * a.page_size));
+      ring.rows[at * kTile + lane + 32 * i] = key < lk ? row : kNoRow;
+      if constexpr (kQ8) {
+        if (key < lk) {
+          // the words that hold the key's scale bytes (never past the arrays' ends)
+          const uint32_t to = ring.scales + (at * kTile + lane + 32 * i) * 16;
+          const long long o = ((long long)row * a.Hkv + (kPair ? 2 : 1) * head) & ~3LL;
+          const int n0 = (int)min(4LL, a.scale_bytes - o), n1 = (int)max(0LL, min(4LL, a.scale_bytes - o - 4));
+          cp_async4(to, a.k_scales + o, n0);
+          cp_async4(to + 8, a.v_scales + o, n0);
+          if constexpr (kPair) {
+            cp_async4(to + 4, a.k_scales + (n1 ? o + 4 : o), n1);
+            cp_async4(to + 12, a.v_scales + (n1 ? o + 4 : o), n1);
+          }
+        }
+      }
+    }
+    if (lane == 0) ring.tile[at] = head;
+    if constexpr (kQ8) cp_async_arrive(ring.full + at);
+    mbar_arrive_warp(ring.full + at);
+    ++c;
+  };
+  int b, head, t0, t1, lk;
+  while (ok && next(b, head, t0, t1, lk)) {
+    const int32_t* table = a.table + (size_t)b * a.max_pages;
+    int page[4], ahead[4];
+    auto look_up = [&](int t, int(&x)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = t * kTile + lane + 32 * i;
+        x[i] = t < t1 && key < lk ? __ldg(table + page_index(a, key)) : 0;
+      }
+    };
+    look_up(t0, ahead);
+#pragma unroll 1
+    for (int t = t0; ok && t < t1; ++t) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) page[i] = ahead[i];
+      look_up(t + 1, ahead);
+      publish(page, t * kTile, lk, head);
+    }
+  }
+  if (ok) {
+    const int none[4] = {0, 0, 0, 0};
+    publish(none, 0, 0, -1);
+  }
+  if constexpr (kQ8) cp_async_wait_all();
+  return ok;
+}
+
+// ----------------------------------------------------------------------------- host side
+
+inline PagedArgs paged_args(const PagedLaunch& L) {
+  PagedArgs a{};
+  a.k_pages = static_cast<const uint8_t*>(L.k_pages);
+  a.v_pages = static_cast<const uint8_t*>(L.v_pages);
+  a.q = static_cast<const __nv_bfloat16*>(L.q);
+  a.q_stride = L.q_stride;
+  a.o = static_cast<__nv_bfloat16*>(L.o);
+  a.lse = L.lse;
+  a.lse_head = L.lse_head;
+  a.lse_row = L.lse_row;
+  a.cu_q = L.cu_q;
+  a.table = L.table;
+  a.seqlens = L.seqlens;
+  a.k_scales = L.k_scales;
+  a.v_scales = L.v_scales;
+  a.status = static_cast<int*>(L.workspace);
+  a.B = L.B;
+  a.Hq = L.Hq;
+  a.Hkv = L.Hkv;
+  a.G = L.Hq / L.Hkv;
+  a.total_q = L.total_q;
+  a.max_q = L.max_q;
+  a.max_k = L.max_k;
+  a.num_pages = L.num_pages;
+  a.page_size = L.page_size;
+  while ((1LL << a.page_shift) < L.page_size) ++a.page_shift;
+  a.page_mul = (uint32_t)((((1ull << a.page_shift) - (unsigned)L.page_size) << 32) / (unsigned)L.page_size + 1);
+  a.max_pages = L.max_pages;
+  a.scale_bytes = (long long)L.num_pages * L.page_size * L.Hkv;
+  a.causal = L.causal;
+  a.scale_log2 = L.scale * 1.4426950408889634f;
+  a.timeout_ns = L.timeout_ns;
+  return a;
+}
+
+// Partial states of `ctas` CTAs, n rows of d dims a unit, behind the status word.
+struct PagedCarve {
+  size_t meta, rows, m, l, lr, o, bytes;
+  void place(PagedArgs& a, void* workspace) const {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.meta = reinterpret_cast<int4*>(ws + meta);
+    a.part_rows = reinterpret_cast<int*>(ws + rows);
+    a.part_m = reinterpret_cast<float*>(ws + m);
+    a.part_l = reinterpret_cast<float*>(ws + l);
+    a.part_lr = reinterpret_cast<float*>(ws + lr);
+    a.part_o = reinterpret_cast<float*>(ws + o);
+  }
+};
+inline PagedCarve paged_carve(int ctas, int n, int d) {
+  PagedCarve c;
+  size_t at = kStatusBytes;
+  auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at += (bytes + 255) & ~size_t(255);
+    return x;
+  };
+  c.meta = take(sizeof(int4) * ctas);
+  c.rows = take(sizeof(int) * ctas * n);
+  c.m = take(sizeof(float) * 2 * ctas * n);
+  c.l = take(sizeof(float) * 2 * ctas * n);
+  c.lr = take(sizeof(float) * 2 * ctas * n);
+  c.o = take(sizeof(float) * 2 * ctas * n * d);
+  c.bytes = at;
+  return c;
+}
+
+}  // namespace paged
+
+}  // namespace fa

@@ -62,20 +62,15 @@
 //  * Few waits: the issue order Q K^T of tile c + 1, then P V of tile c, makes the scores'
 //    barrier of a tile imply that the products of two tiles before have read their
 //    weights, and the weights' barrier that the scores have been read.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
-#include "fa_internal.h"
-#include "ptx.cuh"
+#include "paged_common.cuh"
 
 namespace fa {
+
+using namespace paged;
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 128;  // keys per tile
-constexpr uint32_t kNoRow = 0xFFFFFFFFu;  // past the sequence's end
-
 // Exponent offset and threshold of the running maximum, log2 units.  8 bit: weights
 // up to 2^(7 + 1) use e4m3's range (448) and leave the second piece a floor of
 // 2^-10 / 2^7.  bf16: as in the dense forward.
@@ -109,74 +104,6 @@ struct PagedLayout {
   static constexpr int kCols = kQ8 ? 2 * N : N;  // columns of a product: rows, in 8 bits two pieces of each
   static constexpr uint32_t kTmemCols = (N == 16 ? 64 : (N == 32 ? 128 : 256)) * (kQ8 ? 2 : 1);  // S, S, O
 };
-
-struct PagedArgs {
-  const uint8_t* k_pages;
-  const uint8_t* v_pages;
-  const __nv_bfloat16* q;
-  long long q_stride;  // elements between tokens
-  __nv_bfloat16* o;
-  float* lse;
-  long long lse_head, lse_row;  // strides of lse
-  const int32_t* cu_q;          // null: one token per sequence
-  const int32_t* table;
-  const int32_t* seqlens;
-  const uint8_t* k_scales;
-  const uint8_t* v_scales;
-  int* status;
-  int B, Hq, Hkv, G;
-  int team, teams, sets;  // CTAs (key heads, or pairs of them when d = 64) of a team, teams, teams' worths of heads
-  int total_q, max_q, max_k;
-  int num_pages, page_size, max_pages;
-  uint32_t page_mul, page_shift;  // division by page_size
-  int causal;
-  float scale_log2;
-  int4* meta;       // [CTAs]: parts of the unit that begins in this CTA and ends in a later one
-  int* part_rows;   // [CTAs, N] its rows' output rows (-1: none)
-  float* part_m;    // [2 CTAs, N] reference, log2 units
-  float* part_l;    // [2 CTAs, N] sum of the unrounded weights
-  float* part_lr;   // [2 CTAs, N] the sum that divides O
-  float* part_o;    // [2 CTAs, N, 128]
-  unsigned long long timeout_ns;
-};
-
-// Bounded waits, false also when another role of the CTA has given up.  A phase that is
-// complete at the first look costs no more than that look (every lane's, so that nothing
-// has to be handed over).
-__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns,
-                                            volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, timeout_ns) && !*abort_flag;
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns,
-                                          volatile int* abort_flag) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  bool ok = true;
-  if (lane_id() == 0) ok = mbar_wait(bar, parity, timeout_ns) && !*abort_flag;
-  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-}
-
-// Sequence b: new tokens, keys and first packed row; nq = -1 when its offsets do not fit.
-struct SeqInfo {
-  int nq, lk, qoff;
-};
-__device__ __forceinline__ SeqInfo seq_info(const PagedArgs& a, int b) {
-  SeqInfo s;
-  s.lk = max(0, min(a.seqlens[b], a.max_k));
-  if (a.cu_q == nullptr) {
-    s.nq = 1;
-    s.qoff = b;
-    return s;
-  }
-  s.qoff = a.cu_q[b];
-  const int end = a.cu_q[b + 1];
-  if (s.qoff < 0 || end < s.qoff || end > a.total_q) {
-    s.nq = -1;
-    return s;
-  }
-  s.nq = min(end - s.qoff, a.max_q);
-  return s;
-}
 
 // rows of one tile that belong to one key head
 template <int N, int D>
@@ -227,13 +154,6 @@ __device__ __forceinline__ bool next_piece(const PagedArgs& a, Work& w, Piece& p
   return false;
 }
 
-// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, "Division by
-// Invariant Integers using Multiplication", 1994): s = ceil(log2 d), m = floor(2^32 (2^s - d)
-// / d) + 1, n / d = (hi(m n) + n) >> s.
-__device__ __forceinline__ int page_index(const PagedArgs& a, int n) {
-  return (int)((__umulhi(a.page_mul, (uint32_t)n) + (uint32_t)n) >> a.page_shift);
-}
-
 // Run by one warp: the line's length and where this CTA's stretch begins.
 template <int N, int D>
 __device__ __forceinline__ Work find_work(const PagedArgs& a) {
@@ -279,12 +199,6 @@ __device__ __forceinline__ Work find_work(const PagedArgs& a) {
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
   return w;
-}
-
-__device__ __forceinline__ float redux_max(float x) {
-  float m;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
-  return m;
 }
 
 // Does `pred` hold in any of the 128 softmax threads?  (Also their barrier.)
@@ -402,69 +316,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 1) {
     // -------------------------------------------------------------------- page lookup
-    Piece p;
-    uint32_t c = 0;
-    bool ok = true;
-    const long long scale_bytes = (long long)a.num_pages * a.page_size * a.Hkv;
-    auto publish = [&](const int(&page)[4], int key0, int lk, int tile) {
-      const uint32_t at = c % L::kRing;
-      ok = warp_wait(rows_empty + at, ((c / L::kRing) & 1) ^ 1, a.timeout_ns, abort_flag);
-      if (!ok) return;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = key0 + (int)lane + 32 * i;
-        int pg = page[i];
-        if (pg < 0 || pg >= a.num_pages) {  // never read outside the cache
-          atomicExch(a.status, kStatusBadArg);
-          pg = 0;
-        }
-        const uint32_t row = (uint32_t)(pg * a.page_size + (key - page_index(a, key) * a.page_size));
-        ring_rows[at * kTile + lane + 32 * i] = key < lk ? row : kNoRow;
-        if constexpr (kQ8) {
-          if (key < lk) {
-            // the words that hold the key's scale bytes (never past the arrays' ends)
-            const uint32_t to = smem_u32(smem + L::kOffScales) + (at * kTile + lane + 32 * i) * 16;
-            const long long o = ((long long)row * a.Hkv + (D == 64 ? 2 : 1) * tile) & ~3LL;
-            const int n0 = (int)min(4LL, scale_bytes - o), n1 = (int)max(0LL, min(4LL, scale_bytes - o - 4));
-            cp_async4(to, a.k_scales + o, n0);
-            cp_async4(to + 8, a.v_scales + o, n0);
-            if constexpr (D == 64) {
-              cp_async4(to + 4, a.k_scales + (n1 ? o + 4 : o), n1);
-              cp_async4(to + 12, a.v_scales + (n1 ? o + 4 : o), n1);
-            }
-          }
-        }
-      }
-      if (lane == 0) ring_tile[at] = tile;
-      if constexpr (kQ8) cp_async_arrive(rows_full + at);
-      mbar_arrive_warp(rows_full + at);
-      ++c;
-    };
-    while (ok && next_piece<N, D>(a, w, p)) {
-      const int32_t* table = a.table + (size_t)p.b * a.max_pages;
-      int page[4], next[4];
-      auto look_up = [&](int t, int(&x)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = t * kTile + (int)lane + 32 * i;
-          x[i] = t < p.t1 && key < p.s.lk ? __ldg(table + page_index(a, key)) : 0;
-        }
-      };
-      look_up(p.t0, next);
-#pragma unroll 1
-      for (int t = p.t0; ok && t < p.t1; ++t) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) page[i] = next[i];
-        look_up(t + 1, next);
-        publish(page, t * kTile, p.s.lk, p.hg);
-      }
-    }
-    if (ok) {
-      const int none[4] = {0, 0, 0, 0};
-      publish(none, 0, 0, -1);
-    }
+    const PageRing ring{ring_rows, ring_tile, smem_u32(smem + L::kOffScales), rows_full, rows_empty};
+    const bool ok = look_up_pages<L::kRing, kQ8, D == 64>(a, ring, abort_flag, [&](int& b, int& hg, int& t0, int& t1, int& lk) {
+      Piece p;
+      if (!next_piece<N, D>(a, w, p)) return false;
+      b = p.b, hg = p.hg, t0 = p.t0, t1 = p.t1, lk = p.s.lk;
+      return true;
+    });
     if (!ok && lane == 0) give_up();
-    if constexpr (kQ8) cp_async_wait_all();
   } else if (warp == 2 || warp == 3) {
     // -------------------------------------------------------------------- K and V loaders
     const bool is_v = warp == 3;
@@ -951,33 +810,10 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
   }
 }
 
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-
-struct PagedCarve {
-  size_t meta, rows, m, l, lr, o, bytes;
-};
-PagedCarve paged_carve(int ctas, int n) {
-  PagedCarve c;
-  size_t at = kStatusBytes;
-  auto take = [&](size_t b) {
-    const size_t x = at;
-    at += up256(b);
-    return x;
-  };
-  c.meta = take(sizeof(int4) * ctas);
-  c.rows = take(sizeof(int) * ctas * n);
-  c.m = take(sizeof(float) * 2 * ctas * n);
-  c.l = take(sizeof(float) * 2 * ctas * n);
-  c.lr = take(sizeof(float) * 2 * ctas * n);
-  c.o = take(sizeof(float) * 2 * ctas * n * 128);
-  c.bytes = at;
-  return c;
-}
-
-// Rows per tile: the smallest that holds all rows of one key head's longest chunk (two
-// heads' when d = 64), at most 64.
+// Rows per tile: the smallest that holds all rows of one key head's longest chunk that
+// this kernel takes (two heads' when d = 64), at most 64.
 int paged_rows(const PagedLaunch& L) {
-  const long long rows = (long long)L.max_q * (L.Hq / L.Hkv) * (L.d == 64 ? 2 : 1);
+  const long long rows = std::min((long long)L.max_q * (L.Hq / L.Hkv), (long long)L.few_rows) * (L.d == 64 ? 2 : 1);
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
 }
 
@@ -1001,50 +837,16 @@ fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
                                     L::kSmemBytes) == cudaSuccess;
       }))
     return FA_ERR_CUDA;
-  PagedArgs a;
   const int ctas = num_sms();
-  const PagedCarve c = paged_carve(ctas, N);
-  uint8_t* ws = static_cast<uint8_t*>(L0.workspace);
-  a.k_pages = static_cast<const uint8_t*>(L0.k_pages);
-  a.v_pages = static_cast<const uint8_t*>(L0.v_pages);
-  a.q = static_cast<const __nv_bfloat16*>(L0.q);
-  a.q_stride = L0.q_stride;
-  a.o = static_cast<__nv_bfloat16*>(L0.o);
-  a.lse = L0.lse;
-  a.lse_head = L0.lse_head;
-  a.lse_row = L0.lse_row;
-  a.cu_q = L0.cu_q;
-  a.table = L0.table;
-  a.seqlens = L0.seqlens;
-  a.k_scales = L0.k_scales;
-  a.v_scales = L0.v_scales;
-  a.status = reinterpret_cast<int*>(ws);
-  a.B = L0.B;
-  a.Hq = L0.Hq;
-  a.Hkv = L0.Hkv;
-  a.G = L0.Hq / L0.Hkv;
+  PagedArgs a = paged_args(L0);
+  const PagedCarve c = paged_carve(ctas, N, 128);
   const int groups = D == 64 ? (L0.Hkv + 1) / 2 : L0.Hkv;
   a.team = team_size(groups, ctas);
   a.teams = ctas / a.team;
   a.sets = groups / a.team;
-  a.total_q = L0.total_q;
-  a.max_q = L0.max_q;
-  a.max_k = L0.max_k;
-  a.num_pages = L0.num_pages;
-  a.page_size = L0.page_size;
-  a.page_shift = 0;
-  while ((1LL << a.page_shift) < L0.page_size) ++a.page_shift;
-  a.page_mul = (uint32_t)((((1ull << a.page_shift) - (unsigned)L0.page_size) << 32) / (unsigned)L0.page_size + 1);
-  a.max_pages = L0.max_pages;
-  a.causal = L0.causal;
-  a.scale_log2 = L0.scale * 1.4426950408889634f;
-  a.meta = reinterpret_cast<int4*>(ws + c.meta);
-  a.part_rows = reinterpret_cast<int*>(ws + c.rows);
-  a.part_m = reinterpret_cast<float*>(ws + c.m);
-  a.part_l = reinterpret_cast<float*>(ws + c.l);
-  a.part_lr = reinterpret_cast<float*>(ws + c.lr);
-  a.part_o = reinterpret_cast<float*>(ws + c.o);
-  a.timeout_ns = L0.timeout_ns;
+  a.min_rows = 0;
+  a.max_rows = L0.few_rows;
+  c.place(a, L0.workspace);
   prof_before(stream, kKPaged);
   paged_kernel<N, kQ8, D><<<a.teams * a.team, kThreads, L::kSmemBytes, stream>>>(a);
   cudaError_t err = cudaGetLastError();
@@ -1067,9 +869,9 @@ fa_status launch_paged_rows(const PagedLaunch& L, cudaStream_t stream) {
 
 }  // namespace
 
-size_t paged_workspace_bytes() { return paged_carve(num_sms(), 64).bytes; }
+size_t paged_few_workspace(int rows) { return paged_carve(num_sms(), rows <= 16 ? 16 : (rows <= 32 ? 32 : 64), 128).bytes; }
 
-fa_status launch_paged(const PagedLaunch& L, cudaStream_t stream) {
+fa_status launch_paged_few(const PagedLaunch& L, cudaStream_t stream) {
   switch (paged_rows(L)) {
     case 16: return launch_paged_rows<16>(L, stream);
     case 32: return launch_paged_rows<32>(L, stream);
