@@ -13,15 +13,17 @@
 //  * Keys.  Pages are looked up by the warp of paged_common.cuh; four loader warps fill
 //    the K and V tiles, each 32 keys of every tile.  bf16: 16-byte asynchronous copies.
 //    8 bit: each lane loads 16 codes, multiplies by the row's scale and stores 16 bf16
-//    values.  A code times its power of two is a bf16 number, so the scores and products
-//    are those of the bf16 kernel on the dequantised cache, bit for bit, and the softmax
-//    warps, which bound the kernel, have nothing to add.
+//    values, all of the tile times 2^-60, which the softmax scale and the final 1 / l make
+//    up for.  A code times its power of two is a bf16 number, so the softmax warps, which
+//    bound the kernel, have nothing to add.  The conversion is integer shifts and one bf16
+//    multiplication per pair of codes (dequantise2); through the conversion instructions it
+//    took 7400 cycles of a loader warp per tile, and twice the softmax warps' time with it.
 //  * Work split: the line of all units' tiles, causal ones counted, is cut into equal
 //    parts, one per CTA (one CTA per SM).  A unit cut by a border leaves fp32 partial
 //    states of its 256 rows, two at most per CTA, which a second kernel joins in order.
 //    512 tokens over 16K keys (8 key heads, G = 4) are 64 units for 148 CTAs.
 //  * Warp roles (512 threads): 0 MMA issuer, 1 page lookup, 4-7 loaders, 8-11 and 12-15
-//    the softmax groups of the two row tiles; setmaxnreg 56 / 72 / 192 / 192.
+//    the softmax groups of the two row tiles.
 #include "paged_common.cuh"
 
 namespace fa {
@@ -31,11 +33,19 @@ using namespace paged;
 namespace {
 
 constexpr int kThreads = 512;
-constexpr uint32_t kRegsIssue = 56, kRegsLoad = 72, kRegsSoftmax = 192;
-static_assert(kRegsIssue + kRegsLoad + 2 * kRegsSoftmax <= 4 * 128, "register split exceeds the launch budget");
+// registers per thread of the four warpgroups, out of 4 x 128
+template <bool kQ8>
+constexpr uint32_t kRegsIssue = kQ8 ? 72 : 88;
+template <bool kQ8>
+constexpr uint32_t kRegsLoad = kQ8 ? 72 : 56;
+constexpr uint32_t kRegsSoftmax = 184;
+static_assert(kRegsIssue<true> + kRegsLoad<true> + 2 * kRegsSoftmax <= 4 * 128 &&
+                  kRegsIssue<false> + kRegsLoad<false> + 2 * kRegsSoftmax <= 4 * 128,
+              "register split exceeds the launch budget");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kUnitRows = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr float kTwo60 = 1152921504606846976.f;
 __host__ __device__ constexpr uint32_t tm_s(int t) { return t * 128u; }
 template <int D>
 __host__ __device__ constexpr uint32_t tm_o(int t) {
@@ -56,22 +66,25 @@ struct ChunkLayout {
   // kv_full[S], kv_empty[S], rows_full[R], rows_empty[R], q_full[2], s_full[2], p_half[2], p_full[2], o_done[2]
   static constexpr int kNumBars = 2 * kStages + 2 * kRing + 10;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffWalk = (kOffMisc + 80 + 15) & ~15;
-  static constexpr int kSmemBytes = kOffWalk + 8 * 160 + 1024;  // + alignment slack
+  static constexpr int kPlaceBytes = 96;
+  static constexpr int kOffPlaces = (kOffMisc + 8 + 15) & ~15;  // of the MMA, lookup and softmax warps
+  static constexpr int kSmemBytes = kOffPlaces + 10 * kPlaceBytes + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory of one SM");
 };
 
+// This CTA's stretch [pos, end) of the line of tiles: it begins at tile t of unit `unit` of
+// head hk of sequence b.
 struct Work {
   long long pos, end, total;
-  int b, off;
-  int ctas;
+  int b, hk, unit, t;
+  int ctas;  // CTAs that have a stretch
 };
 
 // Keys that rows up to `row` of a unit's sequence see, and the tiles of them (one, fully
 // masked, when there are none).
 __device__ __forceinline__ int keys_of(const PagedArgs& a, const SeqInfo& s, int row) {
   if (!a.causal) return s.lk;
-  const int token = min(row / a.G, s.nq - 1);
+  const int token = min(token_of_row(a, row), s.nq - 1);
   return max(0, min(s.lk, s.lk - s.nq + token + 1));
 }
 __device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kTile - 1) / kTile); }
@@ -82,110 +95,149 @@ __device__ __forceinline__ int units_of(const PagedArgs& a, int nq) {
 __device__ __forceinline__ int unit_tiles(const PagedArgs& a, const SeqInfo& s, int u) {
   return tiles_of(keys_of(a, s, u * kUnitRows + kUnitRows - 1));
 }
-// Tiles of one key head of a sequence: all its units'.
-__device__ __forceinline__ int head_tiles(const PagedArgs& a, const SeqInfo& s) {
-  const int units = units_of(a, s.nq);
-  if (!a.causal) return units * tiles_of(s.lk);
-  int n = 0;
-  for (int u = 0; u < units; ++u) n += unit_tiles(a, s, u);
-  return n;
-}
-
 struct Piece {
   int b, hk, unit, t0, t1, tiles;
   SeqInfo s;
 };
-// The sequences' head_tiles are only recomputed when the stretch enters a sequence
-// (w.off < 0: not yet).
-struct Walk {
-  Work w;
-  SeqInfo s;
-  int hk, unit, t;  // where pos is
-  bool inside;
-};
-__device__ __forceinline__ void enter(const PagedArgs& a, Walk& k) {
-  // from w.off tiles into sequence w.b
-  k.s = seq_info(a, k.w.b);
-  const int per_head = head_tiles(a, k.s);
-  k.hk = per_head ? k.w.off / per_head : 0;
-  int rest = k.w.off - k.hk * per_head;
-  k.unit = 0;
-  const int units = units_of(a, k.s.nq);
-  while (k.unit < units) {
-    const int n = unit_tiles(a, k.s, k.unit);
-    if (rest < n) break;
-    rest -= n;
-    ++k.unit;
+__device__ __forceinline__ bool next_piece(const PagedArgs& a, Work& w, Piece& p) {
+  if (w.pos >= w.end) return false;
+  p.s = seq_info(a, w.b);
+  while (w.hk >= a.Hkv || p.s.nq <= 0) {  // past the sequence's last head: the next sequence with rows
+    if (++w.b >= a.B) return false;
+    p.s = seq_info(a, w.b);
+    w.hk = w.unit = w.t = 0;
   }
-  k.t = rest;
-  k.inside = true;
-}
-__device__ __forceinline__ bool next_piece(const PagedArgs& a, Walk& k, Piece& p) {
-  if (k.w.pos >= k.w.end) return false;
-  if (!k.inside) enter(a, k);
-  while (k.hk >= a.Hkv || units_of(a, k.s.nq) == 0) {  // past the sequence's last head: the next sequence with rows
-    if (++k.w.b >= a.B) return false;
-    k.s = seq_info(a, k.w.b);
-    k.hk = k.unit = k.t = 0;
-  }
-  p.s = k.s;
-  p.b = k.w.b;
-  p.hk = k.hk;
-  p.unit = k.unit;
-  p.tiles = unit_tiles(a, k.s, k.unit);
-  p.t0 = k.t;
-  p.t1 = (int)min((long long)p.tiles, k.t + (k.w.end - k.w.pos));
-  k.w.pos += p.t1 - p.t0;
-  k.t = p.t1;
-  if (k.t == p.tiles) {
-    k.t = 0;
-    if (++k.unit == units_of(a, k.s.nq)) {
-      k.unit = 0;
-      ++k.hk;
+  p.b = w.b;
+  p.hk = w.hk;
+  p.unit = w.unit;
+  p.tiles = unit_tiles(a, p.s, w.unit);
+  p.t0 = w.t;
+  p.t1 = (int)min((long long)p.tiles, w.t + (w.end - w.pos));
+  w.pos += p.t1 - p.t0;
+  w.t = p.t1;
+  if (w.t == p.tiles) {
+    w.t = 0;
+    if (++w.unit == units_of(a, p.s.nq)) {
+      w.unit = 0;
+      ++w.hk;
     }
   }
   return true;
 }
 
-// Run by one warp: the line's length and where this CTA's stretch begins.
+// A warp's place in the line and its piece.  They lie in shared memory, moved on by lane 0,
+// so that the roles' loops keep their registers.
+struct Place {
+  Work w;
+  Piece p;
+};
+__device__ __forceinline__ bool next_place(const PagedArgs& a, Place* at) {
+  Work w = at->w;
+  Piece p;
+  if (!next_piece(a, w, p)) return false;
+  at->w = w;
+  at->p = p;
+  return true;
+}
+
+__device__ __forceinline__ int warp_sum(int x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
+}
+
+// Run by one warp: the line's length and where this CTA's stretch begins.  The lanes take
+// the units of a sequence (few sequences, long chunks) or the sequences (many).
 __device__ __forceinline__ Work find_work(const PagedArgs& a) {
   const int lane = lane_id();
   Work w;
-  auto cost_of = [&](int b) {
-    if (b >= a.B) return 0;
+  // tiles of one key head: by the whole warp
+  auto head_tiles = [&](const SeqInfo& s) {
+    int n = 0;
+    const int units = units_of(a, s.nq);
+    for (int u = lane; u < units; u += 32) n += unit_tiles(a, s, u);
+    return warp_sum(n);
+  };
+  // the same by one lane
+  auto tiles_alone = [&](const SeqInfo& s) {
+    int n = 0;
+    const int units = units_of(a, s.nq);
+    for (int u = 0; u < units; ++u) n += unit_tiles(a, s, u);
+    return n;
+  };
+  const bool by_units = a.B < 32;
+  auto info = [&](int b) {
     const SeqInfo s = seq_info(a, b);
     if (s.nq < 0 && blockIdx.x == 0) atomicExch(a.status, kStatusBadArg);
-    return s.nq > 0 ? head_tiles(a, s) * a.Hkv : 0;
+    return s;
   };
   long long total = 0;
-  for (int b = lane; b < a.B; b += 32) total += cost_of(b);
+  if (by_units) {
+    for (int b = 0; b < a.B; ++b) total += (long long)head_tiles(info(b)) * a.Hkv;
+  } else {
+    for (int b = lane; b < a.B; b += 32) total += (long long)tiles_alone(info(b)) * a.Hkv;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  }
   w.total = total;
   w.ctas = (int)min((long long)gridDim.x, total);
-  w.b = 0;
-  w.off = 0;
+  w.b = w.hk = w.unit = w.t = 0;
   w.pos = w.end = 0;
   if ((int)blockIdx.x >= w.ctas) return w;
   w.pos = total * blockIdx.x / w.ctas;
   w.end = total * (blockIdx.x + 1) / w.ctas;
+  // the sequence
   long long before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int mine = cost_of(b0 + lane);
-    long long upto = mine;
+  int per_head = 0;
+  if (by_units) {
+    for (;; ++w.b) {
+      per_head = head_tiles(seq_info(a, w.b));
+      if (before + (long long)per_head * a.Hkv > w.pos) break;
+      before += (long long)per_head * a.Hkv;
+    }
+  } else {
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int alone = b0 + lane < a.B ? tiles_alone(seq_info(a, b0 + lane)) : 0;
+      const long long mine = (long long)alone * a.Hkv;
+      long long upto = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += x;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, before + upto > w.pos);
+      if (hit != 0) {
+        const int src = __ffs(hit) - 1;
+        w.b = b0 + src;
+        before += __shfl_sync(0xffffffffu, upto - mine, src);
+        per_head = __shfl_sync(0xffffffffu, alone, src);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  // the head, then the unit
+  const SeqInfo s = seq_info(a, w.b);
+  int rest = (int)(w.pos - before);
+  w.hk = rest / per_head;
+  rest -= w.hk * per_head;
+  const int units = units_of(a, s.nq);
+  for (int u0 = 0; u0 < units; u0 += 32) {
+    const int mine = u0 + lane < units ? unit_tiles(a, s, u0 + lane) : 0;
+    int upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+      const int x = __shfl_up_sync(0xffffffffu, upto, off);
       if (lane >= off) upto += x;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + upto > w.pos);
+    const unsigned hit = __ballot_sync(0xffffffffu, upto > rest);
     if (hit != 0) {
       const int src = __ffs(hit) - 1;
-      w.b = b0 + src;
-      w.off = (int)(w.pos - (before + __shfl_sync(0xffffffffu, upto - mine, src)));
+      w.unit = u0 + src;
+      w.t = rest - __shfl_sync(0xffffffffu, upto - mine, src);
       break;
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    rest -= __shfl_sync(0xffffffffu, upto, 31);
   }
   return w;
 }
@@ -211,13 +263,19 @@ __device__ __forceinline__ void issue_pv_half(uint32_t o_tmem, uint32_t p_tmem, 
   }
 }
 
-// Four e4m3 codes times f, as bf16 (exact).
-__device__ __forceinline__ uint2 scaled_codes(uint32_t q, float f) {
-  const float2 x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q & 0xFFFFu), __NV_E4M3)));
-  const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q >> 16), __NV_E4M3)));
-  const float2 f2 = make_float2(f, f);
-  const float2 xs = fmul2(x, f2), ys = fmul2(y, f2);
-  return make_uint2(pack_bf16x2(xs.x, xs.y), pack_bf16x2(ys.x, ys.y));
+// Two e4m3 codes times 2^e as bf16, times 2^-60, from t with the codes in its high bytes
+// (bits 8-15 and 24-31) and f = 2^(e + 60) twice.  A code's 7 magnitude bits, moved down by
+// 4, are a bf16 number 2^120 too small, subnormal codes included, so one exact
+// multiplication is left: by 2^(e + 120), of which bf16 holds 2^(e + 60) for every e in
+// [-60, 60].  (Products under 2^-126, of rows with a scale under 2^-57, lose bits.)
+__device__ __forceinline__ uint32_t dequantise2(uint32_t t, uint32_t f) {
+  const uint32_t x = (t & 0x80008000u) | ((t >> 4) & 0x07F007F0u);
+  uint32_t y;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f));
+  return y;
+}
+__device__ __forceinline__ uint2 dequantise4(uint32_t q, uint32_t f) {
+  return make_uint2(dequantise2(__byte_perm(q, 0, 0x1404), f), dequantise2(__byte_perm(q, 0, 0x3424), f));
 }
 
 template <int D, bool kQ8>
@@ -238,15 +296,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
   volatile int* ring_tile = reinterpret_cast<volatile int*>(smem + L::kOffTile);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
-  Work* work = reinterpret_cast<Work*>(smem + (L::kOffMisc + 15) / 8 * 8);
   const uint32_t warp = warp_id(), lane = lane_id();
+  // warps 0, 1 and 8 .. 15
+  static_assert(sizeof(Place) <= L::kPlaceBytes, "a place fits");
+  auto place_of = [&](uint32_t x) { return reinterpret_cast<Place*>(smem + L::kOffPlaces + (x < 2 ? x : x - 6) * L::kPlaceBytes); };
 
   if (warp == 8) {
     const Work w = find_work(a);
-    if (lane == 0) {
-      *work = w;
-      a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-    }
+    if (lane < 10) place_of(lane < 2 ? lane : lane + 6)->w = w;
+    if (lane == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -276,23 +334,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk walk;
-  walk.w = *work;
-  walk.inside = false;
+  Place* const place = place_of(warp);
   auto give_up = [&]() {
     *abort_flag = 1;
     atomicCAS(a.status, 0, kStatusTimeout);
   };
 
   if (warp < 4) {
-    regs_dec<kRegsIssue>();
+    regs_dec<kRegsIssue<kQ8>>();
     if (warp == 1) {
       // ------------------------------------------------------------------ page lookup
       const PageRing ring{ring_rows, ring_tile, smem_u32(smem + L::kOffScales), rows_full, rows_empty};
       const bool ok = look_up_pages<L::kRing, kQ8, false>(a, ring, abort_flag, [&](int& b, int& hk, int& t0, int& t1, int& lk) {
-        Piece p;
-        if (!next_piece(a, walk, p)) return false;
+        int more = 0;
+        if (lane == 0) more = next_place(a, place);
+        more = __shfl_sync(0xffffffffu, more, 0);
+        __syncwarp();
+        if (!more) return false;
+        const Piece& p = place->p;
         b = p.b, hk = p.hk, t0 = p.t0, t1 = p.t1, lk = p.s.lk;
+        __syncwarp();
         return true;
       });
       if (!ok && lane == 0) give_up();
@@ -318,12 +379,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
         tc_fence_after();
         return true;
       };
-      Piece p;
-      while (ok && next_piece(a, walk, p)) {
+      while (ok && next_place(a, place)) {
+        const Piece& p = place->p;
+        const int t0 = p.t0, t1 = p.t1;
         // tiles of the unit that each row tile needs; the second may have no row
         const int rows = p.s.nq * a.G - p.unit * kUnitRows;
-        const int nt[2] = {min(p.t1, tiles_of(keys_of(a, p.s, p.unit * kUnitRows + 127))), rows > 128 ? p.t1 : p.t0};
-        bool have[2] = {p.t0 < nt[0], p.t0 < nt[1]};
+        const int nt[2] = {min(t1, tiles_of(keys_of(a, p.s, p.unit * kUnitRows + 127))), rows > 128 ? t1 : t0};
+        bool have[2] = {t0 < nt[0], t0 < nt[1]};
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (t == 0 || rows > 128) {
@@ -343,26 +405,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
           umma_commit(kv_empty + g % L::kStages);
           ++g;
         }
-        for (int j = p.t0; j < p.t1 && ok; ++j) {
+        for (int j = t0; j < t1 && ok; ++j) {
           const uint32_t gv = g++, slot_v = gv % L::kStages;
           if (!slot_ready(gv)) break;
           const SDesc v = SDesc{ring_v.lo + slot_v * kSlot16, ring_v.hi};
-          const bool more = j + 1 < p.t1;
-          SDesc k = ring_k;
+          const bool more = j + 1 < t1;
+          // the next K as well, before the weights are waited for: off the chain of a tile
+          // from its weights to its next scores
+          if (more && !slot_ready(g)) break;
+          const SDesc k = SDesc{ring_k.lo + (g % L::kStages) * kSlot16, ring_k.hi};
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (j < nt[t]) {
               if (!wait(p_half + t, p_cnt[t] & 1)) break;
               tc_fence_after();
-              issue_pv_half<D>(tmem + tm_o<D>(t), tmem + tm_s(t), v, j > p.t0, 0);
+              issue_pv_half<D>(tmem + tm_o<D>(t), tmem + tm_s(t), v, j > t0, 0);
               if (!wait(p_full + t, p_cnt[t] & 1)) break;
               tc_fence_after();
               ++p_cnt[t];
               issue_pv_half<D>(tmem + tm_o<D>(t), tmem + tm_s(t), v, true, 1);
-            }
-            if (t == 0 && more) {
-              if (!slot_ready(g)) break;
-              k = SDesc{ring_k.lo + (g % L::kStages) * kSlot16, ring_k.hi};
             }
             if (more && j + 1 < nt[t]) {
               issue_qk<D>(tmem + tm_s(t), q_desc[t], k);
@@ -383,13 +444,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
       }
     }
   } else if (warp < 8) {
-    regs_dec<kRegsLoad>();
+    regs_dec<kRegsLoad<kQ8>>();
     // ------------------------------------------------------------------ loaders: keys 32 (warp - 4) .. of every tile
     constexpr int kChunks = D * (kQ8 ? 1 : 2) / 16;  // 16-byte pieces of a cache row's slice
     constexpr int kKeys = 32 / kChunks;              // keys per step of the warp
     constexpr int kSteps = 32 / kKeys;
     const uint32_t row_bytes = (uint32_t)a.Hkv * D * (kQ8 ? 1 : 2);
-    const int chunk = lane % kChunks, sub = lane / kChunks, first = (warp - 4) * 32;
+    const int chunk = lane % kChunks, sub = lane / kChunks, first = ((int)warp - 4) * 32;
     const uint32_t ring = smem_u32(ring_rows), words = smem_u32(smem + L::kOffScales);
     bool ok = true;
     for (uint32_t c = 0; ok; ++c) {
@@ -398,47 +459,81 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
       if (!ok) break;
       const int hk = ring_tile[at];
       if (hk < 0) break;
+      // row of key first + i kKeys + sub
+      auto row_of = [&](int i) { return ld_shared_u32(ring + (at * kTile + first + i * kKeys + sub) * 4); };
+      const size_t off = (size_t)hk * D * (kQ8 ? 1 : 2) + chunk * 16;
+      auto slot_of = [&](int kv) { return (2 * c + kv) % L::kStages; };
+      auto wait_empty = [&](int kv) {
+        return warp_wait(kv_empty + slot_of(kv), (((2 * c + kv) / L::kStages) & 1) ^ 1, a.timeout_ns, abort_flag);
+      };
+      if constexpr (kQ8) {
+        // Half of K's steps, the other half, V's halves: each one's codes are loaded while the
+        // one before is converted.  A loop, not unrolled: with all four in line the
+        // loaders and the softmax together outgrew the instruction cache (a third of
+        // all stalls; 512 tokens over 16K keys 262 us).
+        constexpr int kHalf = kSteps / 2;
+        uint4 q[kHalf];
+        auto load = [&](int x, uint4(&to)[kHalf]) {
+          const uint8_t* src = (x >= 2 ? a.v_pages : a.k_pages) + off;
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) {
+            const uint32_t row = row_of((x & 1) * kHalf + i);
+            to[i] = row != kNoRow ? __ldg(reinterpret_cast<const uint4*>(src + (uint64_t)row * row_bytes)) : make_uint4(0, 0, 0, 0);
+          }
+        };
+        load(0, q);
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t g = 2 * c + kv, slot = g % L::kStages;
-        const uint8_t* src = (kv ? a.v_pages : a.k_pages) + (size_t)hk * D * (kQ8 ? 1 : 2) + chunk * 16;
-        const uint32_t tile = smem_u32(smem + L::kOffSlots + slot * L::kTileBytes);
-        uint32_t rw[kSteps];
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) rw[i] = ld_shared_u32(ring + (at * kTile + first + i * kKeys + sub) * 4);
-        if constexpr (kQ8) {
-          uint4 q[kSteps];
-#pragma unroll
-          for (int i = 0; i < kSteps; ++i)
-            q[i] = rw[i] != kNoRow ? __ldg(reinterpret_cast<const uint4*>(src + (uint64_t)rw[i] * row_bytes)) : make_uint4(0, 0, 0, 0);
-          ok = warp_wait(kv_empty + slot, ((g / L::kStages) & 1) ^ 1, a.timeout_ns, abort_flag);
+        for (int x = 0; x < 4; ++x) {
+          const int kv = x >> 1;
+          uint4 next[kHalf];
+          if (x < 3) load(x + 1, next);
+          if ((x & 1) == 0) ok = wait_empty(kv);
           if (!ok) break;
+          const uint32_t tile = smem_u32(smem + L::kOffSlots + slot_of(kv) * L::kTileBytes);
 #pragma unroll
-          for (int i = 0; i < kSteps; ++i) {
-            const int key = first + i * kKeys + sub;
+          for (int i = 0; i < kHalf; ++i) {
+            const uint32_t row = row_of((x & 1) * kHalf + i);
+            const int key = first + ((x & 1) * kHalf + i) * kKeys + sub;
             const uint32_t word = ld_shared_u32(words + (at * kTile + key) * 16 + kv * 8);
-            const uint32_t cut = ((rw[i] * (uint32_t)a.Hkv + hk) & 3u) * 8;
-            const float f = rw[i] != kNoRow ? __uint_as_float(((word >> cut) & 0xFFu) << 23) : 0.f;
-            const uint2 w0 = scaled_codes(q[i].x, f), w1 = scaled_codes(q[i].y, f), w2 = scaled_codes(q[i].z, f),
-                        w3 = scaled_codes(q[i].w, f);
+            const uint32_t cut = ((row * (uint32_t)a.Hkv + hk) & 3u) * 8;
+            // past the sequence's end the codes are zeros, and the word holds anything
+            const uint32_t f = row != kNoRow ? ((((word >> cut) & 0xFFu) + 60u) << 7) * 0x00010001u : 0u;
+            const uint2 w0 = dequantise4(q[i].x, f), w1 = dequantise4(q[i].y, f), w2 = dequantise4(q[i].z, f),
+                        w3 = dequantise4(q[i].w, f);
             const int c2 = 2 * chunk;  // 16-byte chunks of the bf16 row: c2 and c2 + 1
-            const uint32_t row = tile + (c2 >> 3) * L::kBoxBytes + key * 128;
-            st_shared_v4(row + (((c2 & 7) ^ (key & 7)) << 4), w0.x, w0.y, w1.x, w1.y);
-            st_shared_v4(row + ((((c2 & 7) + 1) ^ (key & 7)) << 4), w2.x, w2.y, w3.x, w3.y);
+            const uint32_t to = tile + (c2 >> 3) * L::kBoxBytes + key * 128;
+            st_shared_v4(to + (((c2 & 7) ^ (key & 7)) << 4), w0.x, w0.y, w1.x, w1.y);
+            st_shared_v4(to + ((((c2 & 7) + 1) ^ (key & 7)) << 4), w2.x, w2.y, w3.x, w3.y);
           }
-          fence_proxy_async_smem();
-          mbar_arrive_warp(kv_full + slot);
-        } else {
-          ok = warp_wait(kv_empty + slot, ((g / L::kStages) & 1) ^ 1, a.timeout_ns, abort_flag);
-          if (!ok) break;
+          if (x & 1) {
+            fence_proxy_async_smem();
+            mbar_arrive_warp(kv_full + slot_of(kv));
+          }
 #pragma unroll
-          for (int i = 0; i < kSteps; ++i) {
-            const int key = first + i * kKeys + sub;
-            const bool have = rw[i] != kNoRow;
-            cp_async16_or_zero(tile + (chunk >> 3) * L::kBoxBytes + key * 128 + (((chunk & 7) ^ (key & 7)) << 4),
-                               src + (uint64_t)(have ? rw[i] : 0u) * row_bytes, have);
+          for (int i = 0; i < kHalf; ++i) q[i] = next[i];
+        }
+        if (!ok) break;
+      } else {
+#pragma unroll 1
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          const uint8_t* src = (kv ? a.v_pages : a.k_pages) + off;
+          const uint32_t tile = smem_u32(smem + L::kOffSlots + slot_of(kv) * L::kTileBytes);
+          ok = wait_empty(kv);
+          if (!ok) break;
+#pragma unroll 1
+          for (int i0 = 0; i0 < kSteps; i0 += 8) {
+            uint32_t rw[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) rw[i] = row_of(i0 + i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int key = first + (i0 + i) * kKeys + sub;
+              const bool have = rw[i] != kNoRow;
+              cp_async16_or_zero(tile + (chunk >> 3) * L::kBoxBytes + key * 128 + (((chunk & 7) ^ (key & 7)) << 4),
+                                 src + (uint64_t)(have ? rw[i] : 0u) * row_bytes, have);
+            }
           }
-          cp_async_arrive(kv_full + slot);
+          cp_async_arrive(kv_full + slot_of(kv));
         }
       }
       mbar_arrive_warp(rows_empty + at);
@@ -453,45 +548,42 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
     const int r = quarter * 32 + lane;  // row of the tile
     const uint32_t lanes = (quarter * 32) << 16;
     const uint32_t tS = tmem + lanes + tm_s(t), tO = tmem + lanes + tm_o<D>(t);
+    const float scale_log2 = a.scale_log2 * (kQ8 ? kTwo60 : 1.f);  // the 8 bit tiles are 2^-60 of their values
     uint32_t s_cnt = 0, items = 0;
-    // the warp's place in the line lies in shared memory: registers are for the scores
-    struct Place {
-      Walk walk;
-      Piece p;
-    };
-    static_assert(sizeof(Place) <= 160, "the place fits");
-    Place* place = reinterpret_cast<Place*>(smem + L::kOffWalk + (warp - 8) * 160);
-    if (lane == 0) place->walk = walk;
     for (;;) {
       __syncwarp();
       int more = 0;
-      if (lane == 0) {
-        Walk k = place->walk;
-        Piece q;
-        more = next_piece(a, k, q);
-        if (more) {
-          place->walk = k;
-          place->p = q;
-        }
-      }
+      if (lane == 0) more = next_place(a, place);
       if (__shfl_sync(0xffffffffu, more, 0) == 0) break;
       __syncwarp();
       const Piece& p = place->p;
       const int row0 = p.unit * kUnitRows + t * 128;
       const int rows = p.s.nq * a.G - row0;  // of this tile
       if (rows <= 0) continue;               // (the second tile of a short unit)
-      const int row = row0 + r, token = row / a.G, head = p.hk * a.G + (row - token * a.G);
+      const int row = row0 + r, token = token_of_row(a, row), head = p.hk * a.G + (row - token * a.G);
       const bool mine = r < rows;
-      // Q: every MMA that read the tile has completed (o_done of the piece before)
+      // Q: every MMA that read the tile has completed (o_done of the piece before).  The
+      // warp moves its 32 rows together, D / 8 lanes to a row, so that its loads are whole rows.
+      constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;
+      const uint32_t q_tile = smem_u32(smem) + t * L::kTileBytes;
       {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)(p.s.qoff + token) * a.q_stride + (long long)head * D);
-        const uint32_t dst = smem_u32(smem) + t * L::kTileBytes + r * 128;
-        uint4 x[D / 8];
+        const long long from = mine ? (long long)(p.s.qoff + token) * a.q_stride + (long long)head * D : -1;
+        const int chunk = lane % kLanes, sub = lane / kLanes;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {  // 16 rows at a time
+          uint4 x[16 / kRowsAtOnce];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = mine ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
+            const long long src = __shfl_sync(0xffffffffu, from, h * 16 + i * kRowsAtOnce + sub);
+            x[i] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.q + src) + chunk) : make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          st_shared_v4(dst + (i >> 3) * L::kBoxBytes + (((i & 7) ^ (r & 7)) << 4), x[i].x, x[i].y, x[i].z, x[i].w);
+          for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
+            const int rr = quarter * 32 + h * 16 + i * kRowsAtOnce + sub;
+            st_shared_v4(q_tile + (chunk >> 3) * L::kBoxBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4), x[i].x, x[i].y,
+                         x[i].z, x[i].w);
+          }
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive_warp(q_full + t);
@@ -530,12 +622,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
 #pragma unroll
           for (int c = 0; c < 32; c += 2)
             mxv[i] = fmax3(mxv[i], __uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1]));
-        const float m_tile = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])) * a.scale_log2;
+        const float m_tile = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])) * scale_log2;
         const bool need = (m2 == -INFINITY) || (m_tile > m2 + kRescaleThreshold);
         const float m_use = need ? fmaxf(m2, m_tile) : m2;
         const float alpha = (m2 == -INFINITY) ? 0.f : ex2(m2 - m_use);
         const float m_ref = (m_use == -INFINITY) ? 0.f : m_use;
-        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(-m_ref, -m_ref);
+        const float2 sc2 = make_float2(scale_log2, scale_log2), nm2 = make_float2(-m_ref, -m_ref);
         float2 ex0 = make_float2(0.f, 0.f), ex1 = ex0, rd0 = ex0, rd1 = ex0;  // unrounded and bf16 sums
         auto exp_half = [&](int hf, uint32_t(&pk)[32]) {
 #pragma unroll
@@ -596,29 +688,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
       ++items;
       tc_fence_after();
       const bool whole = p.t0 == 0 && p.t1 == p.tiles;
-      const int out_token = p.s.qoff + (p.unit * kUnitRows + t * 128 + r) / a.G;  // (worked out again rather than kept)
-      const int out_head = p.hk * a.G + (p.unit * kUnitRows + t * 128 + r) % a.G;
+      const int again = p.unit * kUnitRows + t * 128 + r;  // worked out again rather than kept
+      const int out_token = p.s.qoff + token_of_row(a, again);
+      const int out_head = p.hk * a.G + (again - token_of_row(a, again) * a.G);
       const int out_row = mine ? out_token * a.Hq + out_head : -1;
       if (whole) {
-        const float inv = (l > 0.f) ? 1.f / l : (l == 0.f ? 0.f : l);
-        uint4* dst = reinterpret_cast<uint4*>(a.o + (size_t)max(out_row, 0) * D);
+        const float inv = ((l > 0.f) ? 1.f / l : (l == 0.f ? 0.f : l)) * (kQ8 ? kTwo60 : 1.f);
+        const bool none = l == 0.f;  // every key hidden: O = 0, whatever V holds
+        // through the Q tile, whose readers are done, so that the warp stores whole rows
 #pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
           tmem_ld32(tO + cc * 32, o);
           tmem_ld_wait(o);
-          if (mine) {
-            const bool none = l == 0.f;  // every key hidden: O = 0, whatever V holds
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-              const float* f = reinterpret_cast<const float*>(o) + q4 * 8;
-              uint4 x = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
-                                   pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
-              if (none) x = make_uint4(0, 0, 0, 0);
-              dst[cc * 4 + q4] = x;
-            }
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const float* f = reinterpret_cast<const float*>(o) + q4 * 8;
+            uint4 x = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                                 pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
+            if (none) x = make_uint4(0, 0, 0, 0);
+            const int chunk = (cc & 1) * 4 + q4;
+            st_shared_v4(q_tile + (cc >> 1) * L::kBoxBytes + r * 128 + ((chunk ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
           }
         }
+        __syncwarp();
+        const int chunk = lane % kLanes, sub = lane / kLanes;
+#pragma unroll 4
+        for (int i = 0; i < 32; i += kRowsAtOnce) {
+          const int rr = quarter * 32 + i + sub;
+          const int to = __shfl_sync(0xffffffffu, out_row, i + sub);
+          uint4 x;
+          ld_shared_v4(q_tile + (chunk >> 3) * L::kBoxBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4), x.x, x.y, x.z, x.w);
+          if (to >= 0) reinterpret_cast<uint4*>(a.o + (size_t)to * D)[chunk] = x;
+        }
+        __syncwarp();
         if (mine)
           a.lse[out_token * a.lse_row + out_head * a.lse_head] =
               le == 0.f ? -INFINITY : (m2 + __log2f(le)) * 0.69314718055994530942f;
@@ -646,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
         if (p.t0 == 0) {
           a.part_rows[(size_t)blockIdx.x * kUnitRows + t * 128 + r] = out_row;
           if (t == 0 && r == 0) {
-            const Work& w = place->walk.w;
+            const Work& w = place->w;
             const long long last = w.pos - p.t1 + p.tiles - 1;  // the unit's last tile
             a.meta[blockIdx.x] =
                 make_int4((int)(((last + 1) * w.ctas - 1) / w.total) - (int)blockIdx.x + 1, rows > 128 ? 2 : 1, 0, 0);
@@ -701,7 +804,7 @@ __global__ void __launch_bounds__(128) paged_chunk_merge_kernel(const PagedArgs 
     }
   }
   if (row < 0) return;
-  const float inv = lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr);
+  const float inv = (lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr)) * (a.k_scales != nullptr ? kTwo60 : 1.f);
   uint4* dst = reinterpret_cast<uint4*>(a.o + (size_t)row * D + blockIdx.z * 32);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -33,7 +33,8 @@ struct PagedArgs {
   int team, teams, sets;  // CTAs (key heads, or pairs of them when d = 64) of a team, teams, teams' worths of heads
   int total_q, max_q, max_k;
   int num_pages, page_size, max_pages;
-  uint32_t page_mul, page_shift;  // division by page_size
+  uint32_t page_mul, page_shift;    // division by page_size
+  uint32_t group_mul, group_shift;  // and by G
   long long scale_bytes;          // of k_scales, v_scales
   // sequences of min_rows to max_rows rows (new tokens times G) are this kernel's
   int min_rows, max_rows;
@@ -94,6 +95,9 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedArgs& a, int b) {
 // / d) + 1, n / d = (hi(m n) + n) >> s.
 __device__ __forceinline__ int page_index(const PagedArgs& a, int n) {
   return (int)((__umulhi(a.page_mul, (uint32_t)n) + (uint32_t)n) >> a.page_shift);
+}
+__device__ __forceinline__ int token_of_row(const PagedArgs& a, int n) {
+  return (int)((__umulhi(a.group_mul, (uint32_t)n) + (uint32_t)n) >> a.group_shift);
 }
 
 __device__ __forceinline__ float redux_max(float x) {
@@ -212,8 +216,13 @@ inline PagedArgs paged_args(const PagedLaunch& L) {
   a.max_k = L.max_k;
   a.num_pages = L.num_pages;
   a.page_size = L.page_size;
-  while ((1LL << a.page_shift) < L.page_size) ++a.page_shift;
-  a.page_mul = (uint32_t)((((1ull << a.page_shift) - (unsigned)L.page_size) << 32) / (unsigned)L.page_size + 1);
+  auto divide_by = [](unsigned d, uint32_t& mul, uint32_t& shift) {
+    shift = 0;
+    while ((1ull << shift) < d) ++shift;
+    mul = (uint32_t)((((1ull << shift) - d) << 32) / d + 1);
+  };
+  divide_by(L.page_size, a.page_mul, a.page_shift);
+  divide_by(a.G, a.group_mul, a.group_shift);
   a.max_pages = L.max_pages;
   a.scale_bytes = (long long)L.num_pages * L.page_size * L.Hkv;
   a.causal = L.causal;
