@@ -35,9 +35,9 @@ namespace {
 constexpr int kThreads = 512;
 // registers per thread of the four warpgroups, out of 4 x 128
 template <bool kQ8>
-constexpr uint32_t kRegsIssue = kQ8 ? 72 : 88;
+constexpr uint32_t kRegsIssue = kQ8 ? 80 : 88;
 template <bool kQ8>
-constexpr uint32_t kRegsLoad = kQ8 ? 72 : 56;
+constexpr uint32_t kRegsLoad = kQ8 ? 64 : 56;
 constexpr uint32_t kRegsSoftmax = 184;
 static_assert(kRegsIssue<true> + kRegsLoad<true> + 2 * kRegsSoftmax <= 4 * 128 &&
                   kRegsIssue<false> + kRegsLoad<false> + 2 * kRegsSoftmax <= 4 * 128,
@@ -60,20 +60,23 @@ struct ChunkLayout {
   static constexpr int kRing = 8;               // tiles that the page lookup may be ahead
   static constexpr int kOffSlots = 2 * kTileBytes;  // behind the two Q tiles
   static constexpr int kOffScales = kOffSlots + kStages * kTileBytes;
-  static constexpr int kOffRows = kOffScales + kRing * kTile * 16;
+  static constexpr int kOffRows = kOffScales + kRing * kTile * 8;
   static constexpr int kOffTile = kOffRows + kRing * kTile * 4;
   static constexpr int kOffBar = kOffTile + kRing * 4;
-  // kv_full[S], kv_empty[S], rows_full[R], rows_empty[R], q_full[2], s_full[2], p_half[2], p_full[2], o_done[2]
-  static constexpr int kNumBars = 2 * kStages + 2 * kRing + 10;
+  static constexpr int kPieces = 4;  // pieces that the page lookup may be ahead
+  // kv_full[S], kv_empty[S], rows_full[R], rows_empty[R], q_full[2], s_full[2], p_half[2], p_full[2], o_done[2],
+  // piece_full[P], piece_empty[P]
+  static constexpr int kNumBars = 2 * kStages + 2 * kRing + 10 + 2 * kPieces;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kPlaceBytes = 96;
-  static constexpr int kOffPlaces = (kOffMisc + 8 + 15) & ~15;  // of the MMA, lookup and softmax warps
-  static constexpr int kSmemBytes = kOffPlaces + 10 * kPlaceBytes + 1024;  // + alignment slack
+  static constexpr int kPieceBytes = 64;
+  static constexpr int kOffPieces = (kOffMisc + 8 + 15) & ~15;
+  static constexpr int kOffCodes = kOffPieces + kPieces * kPieceBytes;  // 8 bit: the loaders' codes, 128 keys of d
+  static constexpr int kSmemBytes = kOffCodes + kTile * D + 1024;   // + alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory of one SM");
 };
 
-// This CTA's stretch [pos, end) of the line of tiles: it begins at tile t of unit `unit` of
-// head hk of sequence b.
+// This CTA's stretch [pos, end) of the line of tiles: it begins t into what unit `unit` of
+// head hk of sequence b counts.
 struct Work {
   long long pos, end, total;
   int b, hk, unit, t;
@@ -91,53 +94,51 @@ __device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kTile 
 __device__ __forceinline__ int units_of(const PagedArgs& a, int nq) {
   return nq <= 0 ? 0 : (nq * a.G + kUnitRows - 1) / kUnitRows;
 }
-// Tiles of unit u of a key head.
+// A unit's start and end (Q in, O out, the pipeline filled and drained) take about as long as
+// two or three tiles, so each unit counts kUnitCost tiles more, at its beginning: without
+// them the CTAs of many short units (a prompt's first rows) came 13% after the mean.
+constexpr int kUnitCost = 3;
+// Tiles of unit u of a key head, and what it counts.
 __device__ __forceinline__ int unit_tiles(const PagedArgs& a, const SeqInfo& s, int u) {
   return tiles_of(keys_of(a, s, u * kUnitRows + kUnitRows - 1));
 }
+__device__ __forceinline__ int unit_cost(const PagedArgs& a, const SeqInfo& s, int u) {
+  return unit_tiles(a, s, u) + kUnitCost;
+}
 struct Piece {
-  int b, hk, unit, t0, t1, tiles;
+  int b, hk, unit, t0, t1, tiles;  // tiles t0 .. t1 - 1 of the unit's
+  int parts;                       // 0: the whole unit; else, where it begins the unit: parts that it is cut into
   SeqInfo s;
 };
 __device__ __forceinline__ bool next_piece(const PagedArgs& a, Work& w, Piece& p) {
-  if (w.pos >= w.end) return false;
-  p.s = seq_info(a, w.b);
-  while (w.hk >= a.Hkv || p.s.nq <= 0) {  // past the sequence's last head: the next sequence with rows
-    if (++w.b >= a.B) return false;
+  while (w.pos < w.end) {
     p.s = seq_info(a, w.b);
-    w.hk = w.unit = w.t = 0;
-  }
-  p.b = w.b;
-  p.hk = w.hk;
-  p.unit = w.unit;
-  p.tiles = unit_tiles(a, p.s, w.unit);
-  p.t0 = w.t;
-  p.t1 = (int)min((long long)p.tiles, w.t + (w.end - w.pos));
-  w.pos += p.t1 - p.t0;
-  w.t = p.t1;
-  if (w.t == p.tiles) {
-    w.t = 0;
-    if (++w.unit == units_of(a, p.s.nq)) {
-      w.unit = 0;
-      ++w.hk;
+    if (w.hk >= a.Hkv || p.s.nq <= 0) {  // past the sequence's last head, or no rows: the next sequence
+      if (++w.b >= a.B) return false;
+      w.hk = w.unit = w.t = 0;
+      continue;
     }
+    p.b = w.b;
+    p.hk = w.hk;
+    p.unit = w.unit;
+    p.tiles = unit_tiles(a, p.s, w.unit);
+    const int cost = p.tiles + kUnitCost, c0 = w.t, c1 = (int)min((long long)cost, c0 + (w.end - w.pos));
+    p.t0 = max(0, c0 - kUnitCost);
+    p.t1 = max(0, c1 - kUnitCost);
+    w.pos += c1 - c0;
+    // the CTA that has the end of the unit's cost, counted from this one
+    p.parts = c1 < cost || p.t0 > 0 ? (int)(((w.pos + cost - c1) * w.ctas - 1) / w.total) - (int)blockIdx.x + 1 : 0;
+    w.t = c1;
+    if (c1 == cost) {
+      w.t = 0;
+      if (++w.unit == units_of(a, p.s.nq)) {
+        w.unit = 0;
+        ++w.hk;
+      }
+    }
+    if (p.t1 > p.t0) return true;  // else only of what the unit counts more: the next CTA begins it
   }
-  return true;
-}
-
-// A warp's place in the line and its piece.  They lie in shared memory, moved on by lane 0,
-// so that the roles' loops keep their registers.
-struct Place {
-  Work w;
-  Piece p;
-};
-__device__ __forceinline__ bool next_place(const PagedArgs& a, Place* at) {
-  Work w = at->w;
-  Piece p;
-  if (!next_piece(a, w, p)) return false;
-  at->w = w;
-  at->p = p;
-  return true;
+  return false;
 }
 
 __device__ __forceinline__ int warp_sum(int x) {
@@ -151,18 +152,18 @@ __device__ __forceinline__ int warp_sum(int x) {
 __device__ __forceinline__ Work find_work(const PagedArgs& a) {
   const int lane = lane_id();
   Work w;
-  // tiles of one key head: by the whole warp
-  auto head_tiles = [&](const SeqInfo& s) {
+  // what one key head counts: by the whole warp
+  auto head_cost = [&](const SeqInfo& s) {
     int n = 0;
     const int units = units_of(a, s.nq);
-    for (int u = lane; u < units; u += 32) n += unit_tiles(a, s, u);
+    for (int u = lane; u < units; u += 32) n += unit_cost(a, s, u);
     return warp_sum(n);
   };
   // the same by one lane
-  auto tiles_alone = [&](const SeqInfo& s) {
+  auto cost_alone = [&](const SeqInfo& s) {
     int n = 0;
     const int units = units_of(a, s.nq);
-    for (int u = 0; u < units; ++u) n += unit_tiles(a, s, u);
+    for (int u = 0; u < units; ++u) n += unit_cost(a, s, u);
     return n;
   };
   const bool by_units = a.B < 32;
@@ -173,9 +174,9 @@ __device__ __forceinline__ Work find_work(const PagedArgs& a) {
   };
   long long total = 0;
   if (by_units) {
-    for (int b = 0; b < a.B; ++b) total += (long long)head_tiles(info(b)) * a.Hkv;
+    for (int b = 0; b < a.B; ++b) total += (long long)head_cost(info(b)) * a.Hkv;
   } else {
-    for (int b = lane; b < a.B; b += 32) total += (long long)tiles_alone(info(b)) * a.Hkv;
+    for (int b = lane; b < a.B; b += 32) total += (long long)cost_alone(info(b)) * a.Hkv;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   }
@@ -191,13 +192,13 @@ __device__ __forceinline__ Work find_work(const PagedArgs& a) {
   int per_head = 0;
   if (by_units) {
     for (;; ++w.b) {
-      per_head = head_tiles(seq_info(a, w.b));
+      per_head = head_cost(seq_info(a, w.b));
       if (before + (long long)per_head * a.Hkv > w.pos) break;
       before += (long long)per_head * a.Hkv;
     }
   } else {
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int alone = b0 + lane < a.B ? tiles_alone(seq_info(a, b0 + lane)) : 0;
+      const int alone = b0 + lane < a.B ? cost_alone(seq_info(a, b0 + lane)) : 0;
       const long long mine = (long long)alone * a.Hkv;
       long long upto = mine;
 #pragma unroll
@@ -223,7 +224,7 @@ __device__ __forceinline__ Work find_work(const PagedArgs& a) {
   rest -= w.hk * per_head;
   const int units = units_of(a, s.nq);
   for (int u0 = 0; u0 < units; u0 += 32) {
-    const int mine = u0 + lane < units ? unit_tiles(a, s, u0 + lane) : 0;
+    const int mine = u0 + lane < units ? unit_cost(a, s, u0 + lane) : 0;
     int upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -279,7 +280,7 @@ __device__ __forceinline__ uint2 dequantise4(uint32_t q, uint32_t f) {
 }
 
 template <int D, bool kQ8>
-__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ PagedArgs a) {
   using L = ChunkLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -292,20 +293,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
   uint64_t* p_half = q_full + 4;
   uint64_t* p_full = q_full + 6;
   uint64_t* o_done = q_full + 8;
+  uint64_t* piece_full = q_full + 10;
+  uint64_t* piece_empty = piece_full + L::kPieces;
   uint32_t* ring_rows = reinterpret_cast<uint32_t*>(smem + L::kOffRows);
   volatile int* ring_tile = reinterpret_cast<volatile int*>(smem + L::kOffTile);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
   const uint32_t warp = warp_id(), lane = lane_id();
-  // warps 0, 1 and 8 .. 15
-  static_assert(sizeof(Place) <= L::kPlaceBytes, "a place fits");
-  auto place_of = [&](uint32_t x) { return reinterpret_cast<Place*>(smem + L::kOffPlaces + (x < 2 ? x : x - 6) * L::kPlaceBytes); };
+  // The lookup warp walks the line and publishes each piece to the MMA issuer and the softmax
+  // warps (tiles = 0 after the last); one copy of the walk keeps the kernel's code small.
+  static_assert(sizeof(Piece) <= L::kPieceBytes, "a piece fits");
+  auto piece_at = [&](uint32_t n) { return reinterpret_cast<Piece*>(smem + L::kOffPieces + n % L::kPieces * L::kPieceBytes); };
 
-  if (warp == 8) {
-    const Work w = find_work(a);
-    if (lane < 10) place_of(lane < 2 ? lane : lane + 6)->w = w;
-    if (lane == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-  }
+  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(kv_full + s, kQ8 ? 4 : 128);  // a loader warp, or each copying lane
@@ -322,6 +322,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
       mbar_init(p_full + t, 4);
       mbar_init(o_done + t, 1);
     }
+    for (int i = 0; i < L::kPieces; ++i) {
+      mbar_init(piece_full + i, 1);
+      mbar_init(piece_empty + i, 9);
+    }
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -334,7 +338,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Place* const place = place_of(warp);
   auto give_up = [&]() {
     *abort_flag = 1;
     atomicCAS(a.status, 0, kStatusTimeout);
@@ -345,17 +348,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
     if (warp == 1) {
       // ------------------------------------------------------------------ page lookup
       const PageRing ring{ring_rows, ring_tile, smem_u32(smem + L::kOffScales), rows_full, rows_empty};
-      const bool ok = look_up_pages<L::kRing, kQ8, false>(a, ring, abort_flag, [&](int& b, int& hk, int& t0, int& t1, int& lk) {
-        int more = 0;
-        if (lane == 0) more = next_place(a, place);
-        more = __shfl_sync(0xffffffffu, more, 0);
-        __syncwarp();
-        if (!more) return false;
-        const Piece& p = place->p;
+      Work w = find_work(a);
+      uint32_t n = 0;
+      bool fine = true;
+      auto publish = [&](const Piece& p) {
+        fine = warp_wait(piece_empty + n % L::kPieces, ((n / L::kPieces) & 1) ^ 1, a.timeout_ns, abort_flag);
+        if (!fine) return;
+        if (lane == 0) *piece_at(n) = p;
+        mbar_arrive_warp(piece_full + n % L::kPieces);
+        ++n;
+      };
+      bool ok = look_up_pages<L::kRing, kQ8, false>(a, ring, abort_flag, [&](int& b, int& hk, int& t0, int& t1, int& lk) {
+        Piece p;
+        const bool more = next_piece(a, w, p);
+        if (!more) p.tiles = 0;
+        publish(p);
         b = p.b, hk = p.hk, t0 = p.t0, t1 = p.t1, lk = p.s.lk;
-        __syncwarp();
-        return true;
+        return more && fine;
       });
+      ok = ok && fine;
       if (!ok && lane == 0) give_up();
     } else if (warp == 0 && lane == 0) {
       // ------------------------------------------------------------------ MMA issuer
@@ -379,8 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
         tc_fence_after();
         return true;
       };
-      while (ok && next_place(a, place)) {
-        const Piece& p = place->p;
+      for (uint32_t n = 0; wait(piece_full + n % L::kPieces, (n / L::kPieces) & 1); ++n) {
+        const Piece& p = *piece_at(n);
+        if (p.tiles == 0) break;
         const int t0 = p.t0, t1 = p.t1;
         // tiles of the unit that each row tile needs; the second may have no row
         const int rows = p.s.nq * a.G - p.unit * kUnitRows;
@@ -441,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (t == 0 || rows > 128) umma_commit(o_done + t);
+        mbar_arrive(piece_empty + n % L::kPieces);
       }
     }
   } else if (warp < 8) {
@@ -453,93 +466,105 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
     const int chunk = lane % kChunks, sub = lane / kChunks, first = ((int)warp - 4) * 32;
     const uint32_t ring = smem_u32(ring_rows), words = smem_u32(smem + L::kOffScales);
     bool ok = true;
-    for (uint32_t c = 0; ok; ++c) {
-      const uint32_t at = c % L::kRing;
-      ok = warp_wait(rows_full + at, (c / L::kRing) & 1, a.timeout_ns, abort_flag);
-      if (!ok) break;
-      const int hk = ring_tile[at];
-      if (hk < 0) break;
-      // row of key first + i kKeys + sub
-      auto row_of = [&](int i) { return ld_shared_u32(ring + (at * kTile + first + i * kKeys + sub) * 4); };
-      const size_t off = (size_t)hk * D * (kQ8 ? 1 : 2) + chunk * 16;
-      auto slot_of = [&](int kv) { return (2 * c + kv) % L::kStages; };
-      auto wait_empty = [&](int kv) {
-        return warp_wait(kv_empty + slot_of(kv), (((2 * c + kv) / L::kStages) & 1) ^ 1, a.timeout_ns, abort_flag);
+    // head of tile c, -1 after the last; row of key first + i kKeys + sub
+    auto head_of = [&](uint32_t c) {
+      ok = warp_wait(rows_full + c % L::kRing, (c / L::kRing) & 1, a.timeout_ns, abort_flag);
+      return ok ? ring_tile[c % L::kRing] : -1;
+    };
+    auto row_of = [&](uint32_t c, int i) { return ld_shared_u32(ring + ((c % L::kRing) * kTile + first + i * kKeys + sub) * 4); };
+    auto tile_of = [&](uint32_t g) { return smem_u32(smem + L::kOffSlots + (g % L::kStages) * L::kTileBytes); };
+    auto wait_empty = [&](uint32_t g) {
+      ok = warp_wait(kv_empty + g % L::kStages, ((g / L::kStages) & 1) ^ 1, a.timeout_ns, abort_flag);
+      return ok;
+    };
+    int hk = head_of(0);
+    if constexpr (kQ8) {
+      // Slot after slot (K, V of tile 0, K of tile 1, ..).  Each lane's 16 codes of a step
+      // come by an asynchronous copy to a place that only it reads, a slot ahead: no
+      // registers held, and the loop stays at one step's instructions.  (Unrolled over a
+      // slot or more, loads in registers, the loaders and the softmax together outgrew
+      // the instruction cache: 8192 tokens 1190 us.)
+      constexpr int kTogether = 2;  // steps converted side by side (one: 981 us; four: as two)
+      const uint32_t codes = smem_u32(smem + L::kOffCodes) + (first * D) + lane * 16;
+      auto copy = [&](uint32_t g, int head, int i) {
+        const uint32_t row = row_of(g >> 1, i);
+        const uint8_t* src = (g & 1 ? a.v_pages : a.k_pages) + (size_t)head * D + chunk * 16;
+        cp_async16_or_zero(codes + i * 512, src + (uint64_t)(row != kNoRow ? row : 0u) * row_bytes, row != kNoRow);
       };
-      if constexpr (kQ8) {
-        // Half of K's steps, the other half, V's halves: each one's codes are loaded while the
-        // one before is converted.  A loop, not unrolled: with all four in line the
-        // loaders and the softmax together outgrew the instruction cache (a third of
-        // all stalls; 512 tokens over 16K keys 262 us).
-        constexpr int kHalf = kSteps / 2;
-        uint4 q[kHalf];
-        auto load = [&](int x, uint4(&to)[kHalf]) {
-          const uint8_t* src = (x >= 2 ? a.v_pages : a.k_pages) + off;
-#pragma unroll
-          for (int i = 0; i < kHalf; ++i) {
-            const uint32_t row = row_of((x & 1) * kHalf + i);
-            to[i] = row != kNoRow ? __ldg(reinterpret_cast<const uint4*>(src + (uint64_t)row * row_bytes)) : make_uint4(0, 0, 0, 0);
-          }
-        };
-        load(0, q);
+      if (hk >= 0) {
 #pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          const int kv = x >> 1;
-          uint4 next[kHalf];
-          if (x < 3) load(x + 1, next);
-          if ((x & 1) == 0) ok = wait_empty(kv);
-          if (!ok) break;
-          const uint32_t tile = smem_u32(smem + L::kOffSlots + slot_of(kv) * L::kTileBytes);
-#pragma unroll
-          for (int i = 0; i < kHalf; ++i) {
-            const uint32_t row = row_of((x & 1) * kHalf + i);
-            const int key = first + ((x & 1) * kHalf + i) * kKeys + sub;
-            const uint32_t word = ld_shared_u32(words + (at * kTile + key) * 16 + kv * 8);
-            const uint32_t cut = ((row * (uint32_t)a.Hkv + hk) & 3u) * 8;
-            // past the sequence's end the codes are zeros, and the word holds anything
-            const uint32_t f = row != kNoRow ? ((((word >> cut) & 0xFFu) + 60u) << 7) * 0x00010001u : 0u;
-            const uint2 w0 = dequantise4(q[i].x, f), w1 = dequantise4(q[i].y, f), w2 = dequantise4(q[i].z, f),
-                        w3 = dequantise4(q[i].w, f);
-            const int c2 = 2 * chunk;  // 16-byte chunks of the bf16 row: c2 and c2 + 1
-            const uint32_t to = tile + (c2 >> 3) * L::kBoxBytes + key * 128;
-            st_shared_v4(to + (((c2 & 7) ^ (key & 7)) << 4), w0.x, w0.y, w1.x, w1.y);
-            st_shared_v4(to + ((((c2 & 7) + 1) ^ (key & 7)) << 4), w2.x, w2.y, w3.x, w3.y);
-          }
-          if (x & 1) {
-            fence_proxy_async_smem();
-            mbar_arrive_warp(kv_full + slot_of(kv));
-          }
-#pragma unroll
-          for (int i = 0; i < kHalf; ++i) q[i] = next[i];
-        }
-        if (!ok) break;
-      } else {
-#pragma unroll 1
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          const uint8_t* src = (kv ? a.v_pages : a.k_pages) + off;
-          const uint32_t tile = smem_u32(smem + L::kOffSlots + slot_of(kv) * L::kTileBytes);
-          ok = wait_empty(kv);
-          if (!ok) break;
-#pragma unroll 1
-          for (int i0 = 0; i0 < kSteps; i0 += 8) {
-            uint32_t rw[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) rw[i] = row_of(i0 + i);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int key = first + (i0 + i) * kKeys + sub;
-              const bool have = rw[i] != kNoRow;
-              cp_async16_or_zero(tile + (chunk >> 3) * L::kBoxBytes + key * 128 + (((chunk & 7) ^ (key & 7)) << 4),
-                                 src + (uint64_t)(have ? rw[i] : 0u) * row_bytes, have);
-            }
-          }
-          cp_async_arrive(kv_full + slot_of(kv));
+        for (int i = 0; i < kSteps; ++i) {
+          copy(0, hk, i);
+          cp_async_commit();
         }
       }
-      mbar_arrive_warp(rows_empty + at);
+#pragma unroll 1
+      for (uint32_t g = 0; hk >= 0; ++g) {
+        const int next = g & 1 ? head_of((g >> 1) + 1) : hk;
+        if (!ok || !wait_empty(g)) break;
+        const uint32_t tile = tile_of(g) + (chunk >> 2) * L::kBoxBytes;
+        const uint32_t word_at = words + (((g >> 1) % L::kRing) * kTile + first + sub) * 8 + (g & 1) * 4;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kSteps; i0 += kTogether) {
+          uint32_t row[kTogether], word[kTogether];
+          uint4 x[kTogether];
+          cp_async_wait<kSteps - kTogether>();
+#pragma unroll
+          for (int j = 0; j < kTogether; ++j) {
+            row[j] = row_of(g >> 1, i0 + j);
+            word[j] = ld_shared_u32(word_at + (i0 + j) * kKeys * 8);
+            ld_shared_v4(codes + (i0 + j) * 512, x[j].x, x[j].y, x[j].z, x[j].w);
+          }
+#pragma unroll
+          for (int j = 0; j < kTogether; ++j) {
+            const int key = first + (i0 + j) * kKeys + sub;
+            const uint32_t cut = ((row[j] * (uint32_t)a.Hkv + hk) & 3u) * 8;
+            // past the sequence's end the codes are zeros, and the word holds anything
+            const uint32_t f = row[j] != kNoRow ? ((((word[j] >> cut) & 0xFFu) + 60u) << 7) * 0x00010001u : 0u;
+            const uint2 w0 = dequantise4(x[j].x, f), w1 = dequantise4(x[j].y, f), w2 = dequantise4(x[j].z, f),
+                        w3 = dequantise4(x[j].w, f);
+            const uint32_t to = tile + key * 128, c2 = 2 * (chunk & 3);  // 16-byte chunks of the bf16 row: c2 and c2 + 1
+            st_shared_v4(to + ((c2 ^ (key & 7)) << 4), w0.x, w0.y, w1.x, w1.y);
+            st_shared_v4(to + (((c2 + 1) ^ (key & 7)) << 4), w2.x, w2.y, w3.x, w3.y);
+          }
+#pragma unroll
+          for (int j = 0; j < kTogether; ++j) {
+            if (next >= 0) copy(g + 1, next, i0 + j);  // (the codes have been read: they were used above)
+            cp_async_commit();
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive_warp(kv_full + g % L::kStages);
+        if (g & 1) mbar_arrive_warp(rows_empty + (g >> 1) % L::kRing);
+        hk = next;
+      }
+    } else {
+#pragma unroll 1
+      for (uint32_t g = 0; hk >= 0; ++g) {
+        const uint8_t* src = (g & 1 ? a.v_pages : a.k_pages) + (size_t)hk * D * 2 + chunk * 16;
+        if (!wait_empty(g)) break;
+        const uint32_t tile = tile_of(g) + (chunk >> 3) * L::kBoxBytes;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kSteps; i0 += 8) {
+          uint32_t rw[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) rw[i] = row_of(g >> 1, i0 + i);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int key = first + (i0 + i) * kKeys + sub;
+            const bool have = rw[i] != kNoRow;
+            cp_async16_or_zero(tile + key * 128 + (((chunk & 7) ^ (key & 7)) << 4), src + (uint64_t)(have ? rw[i] : 0u) * row_bytes, have);
+          }
+        }
+        cp_async_arrive(kv_full + g % L::kStages);
+        if (g & 1) {
+          mbar_arrive_warp(rows_empty + (g >> 1) % L::kRing);
+          hk = head_of((g >> 1) + 1);
+        }
+      }
     }
     if (!ok && lane == 0) give_up();
-    if constexpr (!kQ8) cp_async_wait_all();
+    cp_async_wait_all();
   } else {
     regs_inc<kRegsSoftmax>();
     // ------------------------------------------------------------------ softmax groups
@@ -550,16 +575,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
     const uint32_t tS = tmem + lanes + tm_s(t), tO = tmem + lanes + tm_o<D>(t);
     const float scale_log2 = a.scale_log2 * (kQ8 ? kTwo60 : 1.f);  // the 8 bit tiles are 2^-60 of their values
     uint32_t s_cnt = 0, items = 0;
-    for (;;) {
-      __syncwarp();
-      int more = 0;
-      if (lane == 0) more = next_place(a, place);
-      if (__shfl_sync(0xffffffffu, more, 0) == 0) break;
-      __syncwarp();
-      const Piece& p = place->p;
+    for (uint32_t n = 0;; ++n) {
+      if (!warp_wait(piece_full + n % L::kPieces, (n / L::kPieces) & 1, a.timeout_ns, abort_flag)) {
+        if (lane == 0) give_up();
+        break;
+      }
+      const Piece& p = *piece_at(n);
+      if (p.tiles == 0) break;
       const int row0 = p.unit * kUnitRows + t * 128;
       const int rows = p.s.nq * a.G - row0;  // of this tile
-      if (rows <= 0) continue;               // (the second tile of a short unit)
+      if (rows <= 0) {                       // (the second tile of a short unit)
+        mbar_arrive_warp(piece_empty + n % L::kPieces);
+        continue;
+      }
       const int row = row0 + r, token = token_of_row(a, row), head = p.hk * a.G + (row - token * a.G);
       const bool mine = r < rows;
       // Q: every MMA that read the tile has completed (o_done of the piece before).  The
@@ -687,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
       }
       ++items;
       tc_fence_after();
-      const bool whole = p.t0 == 0 && p.t1 == p.tiles;
+      const bool whole = p.parts == 0;
       const int again = p.unit * kUnitRows + t * 128 + r;  // worked out again rather than kept
       const int out_token = p.s.qoff + token_of_row(a, again);
       const int out_head = p.hk * a.G + (again - token_of_row(a, again) * a.G);
@@ -748,14 +776,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const PagedArg
         a.part_lr[at] = l;
         if (p.t0 == 0) {
           a.part_rows[(size_t)blockIdx.x * kUnitRows + t * 128 + r] = out_row;
-          if (t == 0 && r == 0) {
-            const Work& w = place->w;
-            const long long last = w.pos - p.t1 + p.tiles - 1;  // the unit's last tile
-            a.meta[blockIdx.x] =
-                make_int4((int)(((last + 1) * w.ctas - 1) / w.total) - (int)blockIdx.x + 1, rows > 128 ? 2 : 1, 0, 0);
-          }
+          if (t == 0 && r == 0) a.meta[blockIdx.x] = make_int4(p.parts, rows > 128 ? 2 : 1, 0, 0);
         }
       }
+      mbar_arrive_warp(piece_empty + n % L::kPieces);
       tc_fence_before();  // O is read before the next piece's products overwrite it (q_full orders them)
     }
   }

@@ -109,12 +109,13 @@ __device__ __forceinline__ float redux_max(float x) {
 // A ring of tiles in shared memory, written by the lookup warp: the rows of the flattened
 // pages that hold the tile's keys (kNoRow past the sequence's end), the key head (or pair of
 // heads), -1 after the last tile, and in 8 bits per key the words that hold its K and V
-// scale bytes, two each when the heads of a pair may lie in different words.  `full` counts
+// scale bytes, one each, or two each (K, K, V, V) when the heads of a pair may lie in
+// different words.  `full` counts
 // one arrival, in 8 bits 33; the readers arrive on `empty`.
 struct PageRing {
   uint32_t* rows;
   volatile int* tile;
-  uint32_t scales;  // shared-memory address, 16 bytes per key
+  uint32_t scales;  // shared-memory address
   uint64_t* full;
   uint64_t* empty;
 };
@@ -143,12 +144,13 @@ __device__ __forceinline__ bool look_up_pages(const PagedArgs& a, const PageRing
       ring.rows[at * kTile + lane + 32 * i] = key < lk ? row : kNoRow;
       if constexpr (kQ8) {
         if (key < lk) {
+          constexpr int kWords = kPair ? 2 : 1;
           // the words that hold the key's scale bytes (never past the arrays' ends)
-          const uint32_t to = ring.scales + (at * kTile + lane + 32 * i) * 16;
+          const uint32_t to = ring.scales + (at * kTile + lane + 32 * i) * 8 * kWords;
           const long long o = ((long long)row * a.Hkv + (kPair ? 2 : 1) * head) & ~3LL;
           const int n0 = (int)min(4LL, a.scale_bytes - o), n1 = (int)max(0LL, min(4LL, a.scale_bytes - o - 4));
           cp_async4(to, a.k_scales + o, n0);
-          cp_async4(to + 8, a.v_scales + o, n0);
+          cp_async4(to + 4 * kWords, a.v_scales + o, n0);
           if constexpr (kPair) {
             cp_async4(to + 4, a.k_scales + (n1 ? o + 4 : o), n1);
             cp_async4(to + 12, a.v_scales + (n1 ? o + 4 : o), n1);

@@ -571,7 +571,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         float kf[2] = {1.f, 1.f}, ve[2] = {0.f, 0.f}, vinv[2] = {1.f, 1.f};  // the key's scales, two heads' when d = 64
         if constexpr (kQ8) {
           const uint32_t at = c % L::kRing, rw = ring_rows[at * kTile + r];
-          const uint4 words = reinterpret_cast<const uint4*>(smem + L::kOffScales)[at * kTile + r];
+          uint4 words;
+          if constexpr (D == 64) {
+            words = reinterpret_cast<const uint4*>(smem + L::kOffScales)[at * kTile + r];
+          } else {
+            const uint2 w2 = reinterpret_cast<const uint2*>(smem + L::kOffScales)[at * kTile + r];
+            words = make_uint4(w2.x, 0, w2.y, 0);
+          }
           mbar_arrive_warp(rows_empty + at);
           // byte of the head in its word, and the pair's second head's after it
           const uint32_t cut = ((rw * (uint32_t)a.Hkv + (D == 64 ? 2 : 1) * p.hg) & 3u) * 8;
