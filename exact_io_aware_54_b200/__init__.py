@@ -172,7 +172,7 @@ def workspace(nbytes: int, device, tag: str = "default") -> torch.Tensor:
     return ws
 
 
-_paged_bytes = 0
+_paged_ws: dict = {}  # (device index, stream) -> workspace
 
 
 def paged_workspace(device=None, nbytes: int = 0) -> torch.Tensor:
@@ -182,15 +182,26 @@ def paged_workspace(device=None, nbytes: int = 0) -> torch.Tensor:
     One per stream, since two calls that may run at the same time must not share a
     workspace.  Calls under stream capture get one of their own from the graph's
     memory, so that graphs share it neither with each other nor with eager calls."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    global _paged_bytes
+    index = torch.device(device).index if device is not None else None
+    return _paged_workspace(torch.cuda.current_device() if index is None else index, nbytes)
+
+
+def _paged_workspace(index: int, nbytes: int) -> torch.Tensor:
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+        ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=torch.device("cuda", index))
         ws[:256].zero_()  # the status word; the rest is written before it is read
         return ws
-    if not _paged_bytes:  # what the largest call needs, so that it never has to grow
-        _paged_bytes = fa_paged_workspace_size(1, 64, 1, 4096, 4096, 128)
-    return workspace(max(int(nbytes), _paged_bytes), dev, f"paged:{_stream_ptr(dev)}")
+    key = (index, _raw_stream(index))
+    ws = _paged_ws.get(key)
+    if ws is None:  # as large as any call needs, so that it never has to grow
+        ws = torch.zeros(fa_paged_workspace_size(1, 64, 1, 4096, 4096, 128), dtype=torch.uint8,
+                         device=torch.device("cuda", index))
+        _paged_ws[key] = ws
+    return ws
+
+
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _stream_ptr(device) -> int:
@@ -601,57 +612,84 @@ def fa_decode_paged(q, k_pages, v_pages, block_table, seqlens_k, max_seqlen_k: i
 
 
 # --------------------------------------------------------------------------- paged cache
+#
+# A serving step makes these calls once per layer, so their checks are written to cost
+# little: each tensor is looked at once, and compared by device index.
+
+_BF16, _FP8, _U8, _I32, _F32 = torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.float32
 
 
-def _on_device(t):
-    """Launches go to the current device: make it the tensor's for the call."""
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+def _on_device(index):
+    """Launches go to the current device: make it the tensors' for the call."""
+    return contextlib.nullcontext() if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
-def _check_rows(name, t, H, d):
-    """Packed rows [total, H, d] bf16 whose rows may be further apart than H d (a slice
-    of a fused projection).  Returns elements between rows."""
+def _ptr_of(name, t, dtype, shape, index):
+    """Pointer of a contiguous CUDA tensor of the given type and shape on device `index`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device_of(name, t, dims):
+    """Device index of a CUDA tensor with `dims` dimensions."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != d:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [total, {H}, {d}]")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, has shape {tuple(t.shape)}")
+    return t.get_device()
+
+
+def _rows_of(name, t, total, H, d, index):
+    """Pointer and row stride of packed rows [total, H, d] bf16 whose rows may be further
+    apart than H d (a slice of a fused projection)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
+    if t.dtype is not _BF16:
+        raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
+    if t.shape != (total, H, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(total, H, d)}")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (H > 1 and s1 != d):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return H * d if t.shape[0] == 1 else s0
+    return t.data_ptr(), (H * d if total == 1 else s0)
 
 
-def _check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B, d=None):
-    """Checks a paged cache; returns (num_pages, page_size, H, d, k_scales pointer, v_scales pointer)."""
+def _pages_of(k_pages, v_pages, k_scales, v_scales, block_table, B, index):
+    """Checks a paged cache: (num_pages, page_size, H, d), max_pages_per_seq, and the
+    pointers of pages, scales (None without) and table."""
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise ValueError("k_pages/v_pages must be [num_pages, page_size, H, d]")
-    if (k_scales is None) != (v_scales is None):
-        raise ValueError("k_scales and v_scales are given together or not at all")
-    dtype = torch.bfloat16 if k_scales is None else torch.float8_e4m3fn
-    shape = tuple(k_pages.shape)
-    _check_tensor("k_pages", k_pages, dtype)
-    _check_tensor("v_pages", v_pages, dtype, shape)
+    shape = k_pages.shape
     ks = vs = None
-    if k_scales is not None:
-        _check_tensor("k_scales", k_scales, torch.uint8, shape[:3])
-        _check_tensor("v_scales", v_scales, torch.uint8, shape[:3])
-        ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+    if k_scales is not None and v_scales is not None:
+        dtype, per_row = _FP8, shape[:3]
+        ks = _ptr_of("k_scales", k_scales, _U8, per_row, index)
+        vs = _ptr_of("v_scales", v_scales, _U8, per_row, index)
+    elif k_scales is None and v_scales is None:
+        dtype = _BF16
+    else:
+        raise ValueError("k_scales and v_scales are given together or not at all")
+    kp = _ptr_of("k_pages", k_pages, dtype, shape, index)
+    vp = _ptr_of("v_pages", v_pages, dtype, shape, index)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, max_pages_per_seq]")
-    _check_tensor("block_table", block_table, torch.int32)
-    if d is not None and shape[3] != d:
-        raise ValueError(f"the pages' head dimension is {shape[3]}, expected {d}")
-    return shape + (ks, vs)
+    most = block_table.shape[1]
+    return shape, most, kp, vp, ks, vs, _ptr_of("block_table", block_table, _I32, (B, most), index)
 
 
-def _same_device(t, *others):
-    for x in others:
-        if x is not None and x.device != t.device:
-            raise ValueError(f"tensors on {t.device} and {x.device}")
+def _paged_ws_of(ws, index, nbytes):
+    if ws is None:
+        ws = _paged_workspace(index, nbytes)
+    elif not isinstance(ws, torch.Tensor) or ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous CUDA tensor on cuda:{index}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def fa_cache_write(k, v, k_pages, v_pages, cu_seqlens, block_table, seqlens_k, k_scales=None, v_scales=None,
@@ -662,23 +700,18 @@ def fa_cache_write(k, v, k_pages, v_pages, cu_seqlens, block_table, seqlens_k, k
     torch.float8_e4m3fn with scale bytes k_scales, v_scales [num_pages, page_size, H]
     (uint8): a row's slice of one head stands for codes * 2^(byte - 127)."""
     lib = load()
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1:
-        raise ValueError("cu_seqlens must be [B+1]")
+    index = _device_of("cu_seqlens", cu_seqlens, 1)
     B = cu_seqlens.shape[0] - 1
-    P, page, H, d, ks, vs = _check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B)
-    k_stride, v_stride = _check_rows("k", k, H, d), _check_rows("v", v, H, d)
-    if v.shape != k.shape:
-        raise ValueError("k and v differ in shape")
-    _check_tensor("cu_seqlens", cu_seqlens, torch.int32)
-    _check_tensor("seqlens_k", seqlens_k, torch.int32, (B,))
-    _same_device(k, v, k_pages, v_pages, cu_seqlens, block_table, seqlens_k, k_scales, v_scales, ws)
-    with _on_device(k):
-        if ws is None:
-            ws = paged_workspace(k.device)
-        st = lib.fa_cache_write(k.data_ptr(), v.data_ptr(), k_stride, v_stride, cu_seqlens.data_ptr(),
-                                block_table.data_ptr(), seqlens_k.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                ks, vs, B, H, k.shape[0], P, page, block_table.shape[1], d, ws.data_ptr(),
-                                ws.numel(), _stream_ptr(k.device))
+    (P, page, H, d), most, kp, vp, ks, vs, table = _pages_of(k_pages, v_pages, k_scales, v_scales, block_table, B, index)
+    total = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+    kr, k_stride = _rows_of("k", k, total, H, d, index)
+    vr, v_stride = _rows_of("v", v, total, H, d, index)
+    cu = _ptr_of("cu_seqlens", cu_seqlens, _I32, (B + 1,), index)
+    lens = _ptr_of("seqlens_k", seqlens_k, _I32, (B,), index)
+    with _on_device(index):
+        wp, wn = _paged_ws_of(ws, index, 256)
+        st = lib.fa_cache_write(kr, vr, k_stride, v_stride, cu, table, lens, kp, vp, ks, vs, B, H, total, P, page, most,
+                                d, wp, wn, _raw_stream(index))
     _raise("fa_cache_write", st)
 
 
@@ -688,23 +721,18 @@ def fa_cache_read(k_pages, v_pages, cu_seqlens_k, block_table, total_k: int, k_s
     cu_seqlens_k[b+1] - cu_seqlens_k[b], into rows cu_seqlens_k[b] .. of (k, v)
     [total_k, H, d] bf16, exactly.  Rows that belong to no sequence are left alone."""
     lib = load()
-    if not isinstance(cu_seqlens_k, torch.Tensor) or cu_seqlens_k.dim() != 1:
-        raise ValueError("cu_seqlens_k must be [B+1]")
-    B = cu_seqlens_k.shape[0] - 1
-    P, page, H, d, ks, vs = _check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B)
-    total_k = int(total_k)
-    _check_tensor("cu_seqlens_k", cu_seqlens_k, torch.int32)
-    out_k = torch.empty((total_k, H, d), dtype=torch.bfloat16, device=k_pages.device) if out_k is None else out_k
-    out_v = torch.empty((total_k, H, d), dtype=torch.bfloat16, device=k_pages.device) if out_v is None else out_v
-    _check_tensor("out_k", out_k, torch.bfloat16, (total_k, H, d))
-    _check_tensor("out_v", out_v, torch.bfloat16, (total_k, H, d))
-    _same_device(k_pages, v_pages, cu_seqlens_k, block_table, k_scales, v_scales, out_k, out_v, ws)
-    with _on_device(k_pages):
-        if ws is None:
-            ws = paged_workspace(k_pages.device)
-        st = lib.fa_cache_read(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, cu_seqlens_k.data_ptr(),
-                               block_table.data_ptr(), out_k.data_ptr(), out_v.data_ptr(), B, H, total_k, P, page,
-                               block_table.shape[1], d, ws.data_ptr(), ws.numel(), _stream_ptr(k_pages.device))
+    index = _device_of("cu_seqlens_k", cu_seqlens_k, 1)
+    B, total_k = cu_seqlens_k.shape[0] - 1, int(total_k)
+    (P, page, H, d), most, kp, vp, ks, vs, table = _pages_of(k_pages, v_pages, k_scales, v_scales, block_table, B, index)
+    shape = (total_k, H, d)
+    out_k = k_pages.new_empty(shape, dtype=_BF16) if out_k is None else out_k
+    out_v = k_pages.new_empty(shape, dtype=_BF16) if out_v is None else out_v
+    ok, ov = _ptr_of("out_k", out_k, _BF16, shape, index), _ptr_of("out_v", out_v, _BF16, shape, index)
+    cu = _ptr_of("cu_seqlens_k", cu_seqlens_k, _I32, (B + 1,), index)
+    with _on_device(index):
+        wp, wn = _paged_ws_of(ws, index, 256)
+        st = lib.fa_cache_read(kp, vp, ks, vs, cu, table, ok, ov, B, H, total_k, P, page, most, d, wp, wn,
+                               _raw_stream(index))
     _raise("fa_cache_read", st)
     return out_k, out_v
 
@@ -718,30 +746,26 @@ def fa_fwd_paged(q, k_pages, v_pages, cu_seqlens_q, block_table, seqlens_k, max_
     query head h reads key head h // (Hq / Hkv).  Returns (o [total_q, Hq, d] bf16,
     lse [Hq, total_q] fp32)."""
     lib = load()
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be [total_q, Hq, d]")
+    index = _device_of("q", q, 3)
     total_q, Hq, d = q.shape
     if not isinstance(cu_seqlens_q, torch.Tensor) or cu_seqlens_q.dim() != 1:
         raise ValueError("cu_seqlens_q must be [B+1]")
     B = cu_seqlens_q.shape[0] - 1
-    q_stride = _check_rows("q", q, Hq, d)
-    P, page, Hkv, _, ks, vs = _check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B, d)
-    _check_tensor("cu_seqlens_q", cu_seqlens_q, torch.int32)
-    _check_tensor("seqlens_k", seqlens_k, torch.int32, (B,))
-    out = torch.empty((total_q, Hq, d), dtype=torch.bfloat16, device=q.device) if out is None else out
-    lse = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device) if lse is None else lse
-    _check_tensor("out", out, torch.bfloat16, (total_q, Hq, d))
-    _check_tensor("lse", lse, torch.float32, (Hq, total_q))
-    _same_device(q, k_pages, v_pages, cu_seqlens_q, block_table, seqlens_k, k_scales, v_scales, out, lse, ws)
-    with _on_device(q):
-        if ws is None:
-            ws = paged_workspace(q.device, lib.fa_paged_workspace_size(B, Hq, Hkv, int(max_seqlen_q),
-                                                                       int(max_seqlen_k), d))
-        st = lib.fa_fwd_paged(q.data_ptr(), q_stride, k_pages.data_ptr(), v_pages.data_ptr(), ks, vs,
-                              cu_seqlens_q.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(), out.data_ptr(),
-                              lse.data_ptr(), B, Hq, Hkv, total_q, P, page, block_table.shape[1], int(max_seqlen_q),
-                              int(max_seqlen_k), d, int(bool(causal)), _scale(softmax_scale), ws.data_ptr(),
-                              ws.numel(), _stream_ptr(q.device))
+    qp, q_stride = _rows_of("q", q, total_q, Hq, d, index)
+    (P, page, Hkv, dk), most, kp, vp, ks, vs, table = _pages_of(k_pages, v_pages, k_scales, v_scales, block_table, B, index)
+    if dk != d:
+        raise ValueError(f"the pages' head dimension is {dk}, q's is {d}")
+    cu = _ptr_of("cu_seqlens_q", cu_seqlens_q, _I32, (B + 1,), index)
+    lens = _ptr_of("seqlens_k", seqlens_k, _I32, (B,), index)
+    out = q.new_empty((total_q, Hq, d)) if out is None else out
+    lse = q.new_empty((Hq, total_q), dtype=_F32) if lse is None else lse
+    op = _ptr_of("out", out, _BF16, (total_q, Hq, d), index)
+    lp = _ptr_of("lse", lse, _F32, (Hq, total_q), index)
+    max_q, max_k = int(max_seqlen_q), int(max_seqlen_k)
+    with _on_device(index):
+        wp, wn = _paged_ws_of(ws, index, lib.fa_paged_workspace_size(B, Hq, Hkv, max_q, max_k, d))
+        st = lib.fa_fwd_paged(qp, q_stride, kp, vp, ks, vs, cu, table, lens, op, lp, B, Hq, Hkv, total_q, P, page, most,
+                              max_q, max_k, d, int(bool(causal)), _scale(softmax_scale), wp, wn, _raw_stream(index))
     _raise("fa_fwd_paged", st)
     return out, lse
 
@@ -753,26 +777,24 @@ def fa_decode_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq
     page_size, Hkv] (fa_cache_write); block_table int32 [B, max_pages_per_seq];
     seqlens_k int32 [B].  Returns (o [B, Hq, d] bf16, lse [B, Hq] fp32)."""
     lib = load()
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be [B, Hq, d]")
-    B, Hq, d = q.shape
-    _check_tensor("q", q, torch.bfloat16)
-    if k_scales is None:
+    index = _device_of("q", q, 3)
+    shape = q.shape
+    B, Hq, d = shape
+    qp = _ptr_of("q", q, _BF16, shape, index)
+    if k_scales is None or v_scales is None:
         raise ValueError("k_scales and v_scales are needed")
-    P, page, Hkv, _, ks, vs = _check_pages(k_pages, v_pages, k_scales, v_scales, block_table, B, d)
-    _check_tensor("seqlens_k", seqlens_k, torch.int32, (B,))
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
-    _check_tensor("out", out, torch.bfloat16, (B, Hq, d))
-    _check_tensor("lse", lse, torch.float32, (B, Hq))
-    _same_device(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, out, lse, ws)
-    with _on_device(q):
-        if ws is None:
-            ws = paged_workspace(q.device, lib.fa_paged_workspace_size(B, Hq, Hkv, 1, int(max_seqlen_k), d))
-        st = lib.fa_decode_paged_q8(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ks, vs,
-                                    block_table.data_ptr(), seqlens_k.data_ptr(), B, Hq, Hkv, P, page,
-                                    block_table.shape[1], int(max_seqlen_k), d, _scale(softmax_scale),
-                                    out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr(q.device))
+    (P, page, Hkv, dk), most, kp, vp, ks, vs, table = _pages_of(k_pages, v_pages, k_scales, v_scales, block_table, B, index)
+    if dk != d:
+        raise ValueError(f"the pages' head dimension is {dk}, q's is {d}")
+    lens = _ptr_of("seqlens_k", seqlens_k, _I32, (B,), index)
+    out = q.new_empty(shape) if out is None else out
+    lse = q.new_empty((B, Hq), dtype=_F32) if lse is None else lse
+    op, lp = _ptr_of("out", out, _BF16, shape, index), _ptr_of("lse", lse, _F32, (B, Hq), index)
+    max_k = int(max_seqlen_k)
+    with _on_device(index):
+        wp, wn = _paged_ws_of(ws, index, lib.fa_paged_workspace_size(B, Hq, Hkv, 1, max_k, d))
+        st = lib.fa_decode_paged_q8(qp, kp, vp, ks, vs, table, lens, B, Hq, Hkv, P, page, most, max_k, d,
+                                    _scale(softmax_scale), op, lp, wp, wn, _raw_stream(index))
     _raise("fa_decode_paged_q8", st)
     return out, lse
 

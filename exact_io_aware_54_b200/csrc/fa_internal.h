@@ -247,7 +247,7 @@ struct PagedLaunch {
   unsigned long long timeout_ns;
 };
 fa_status launch_paged_few(const PagedLaunch& a, cudaStream_t stream);
-size_t paged_few_workspace(int rows);
+size_t paged_few_workspace();
 // The same for sequences of many rows (paged_chunk_sm100.cu).
 fa_status launch_paged_chunk(const PagedLaunch& a, cudaStream_t stream);
 size_t paged_chunk_workspace(int d);

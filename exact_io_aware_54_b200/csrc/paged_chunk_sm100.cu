@@ -35,9 +35,9 @@ namespace {
 constexpr int kThreads = 512;
 // registers per thread of the four warpgroups, out of 4 x 128
 template <bool kQ8>
-constexpr uint32_t kRegsIssue = kQ8 ? 80 : 88;
+constexpr uint32_t kRegsIssue = kQ8 ? 64 : 88;
 template <bool kQ8>
-constexpr uint32_t kRegsLoad = kQ8 ? 64 : 56;
+constexpr uint32_t kRegsLoad = kQ8 ? 80 : 56;
 constexpr uint32_t kRegsSoftmax = 184;
 static_assert(kRegsIssue<true> + kRegsLoad<true> + 2 * kRegsSoftmax <= 4 * 128 &&
                   kRegsIssue<false> + kRegsLoad<false> + 2 * kRegsSoftmax <= 4 * 128,

@@ -13,7 +13,7 @@
 //
 // B200 design
 //  * Transposed products.  A tile of 128 keys is the M side: S^T [128 keys, N rows] =
-//    K Q^T and O^T [128 dims, N rows] += V^T P^T, with N = 16, 32 or 64 rows, so a
+//    K Q^T and O^T [128 dims, N rows] += V^T P^T, with N = 16 or 32 rows, so a
 //    tile of few rows does not pay for 128.  Lane of tensor memory = key (then
 //    dim), column = row: a softmax thread owns one key and N scores.
 //  * 8 bit cache without conversion.  K and V tiles stay e4m3 in shared memory and are
@@ -83,7 +83,7 @@ struct SoftmaxRange {
 template <int N, bool kQ8>
 struct PagedLayout {
   static constexpr int kSlotBytes = kTile * 128 * (kQ8 ? 1 : 2);  // one K or V tile
-  static constexpr int kSlots = kQ8 ? (N == 64 ? 9 : (N == 32 ? 11 : 12)) : (N == 64 ? 5 : 6);  // what fits
+  static constexpr int kSlots = kQ8 ? (N == 32 ? 11 : 12) : 6;  // what fits
   static constexpr int kRowBlock = N * 128;      // one 128-byte column block of the N rows
   static constexpr int kOffQ = kSlots * kSlotBytes;  // two e4m3 pieces, or two 64-dim blocks
   static constexpr int kOffP = kOffQ + 2 * kRowBlock;  // double buffer of two e4m3 pieces, or of bf16
@@ -102,7 +102,7 @@ struct PagedLayout {
   static constexpr int kSmemBytes = kOffScales + (kQ8 ? kRing * kTile * 16 : 0) + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory of one SM");
   static constexpr int kCols = kQ8 ? 2 * N : N;  // columns of a product: rows, in 8 bits two pieces of each
-  static constexpr uint32_t kTmemCols = (N == 16 ? 64 : (N == 32 ? 128 : 256)) * (kQ8 ? 2 : 1);  // S, S, O
+  static constexpr uint32_t kTmemCols = (N == 16 ? 64 : 128) * (kQ8 ? 2 : 1);  // S, S, O
 };
 
 // rows of one tile that belong to one key head
@@ -816,11 +816,11 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
   }
 }
 
-// Rows per tile: the smallest that holds all rows of one key head's longest chunk that
-// this kernel takes (two heads' when d = 64), at most 64.
+// Rows per tile: 16 where that holds all rows of one key head's longest chunk that this
+// kernel takes (two heads' when d = 64), else 32.
 int paged_rows(const PagedLaunch& L) {
   const long long rows = std::min((long long)L.max_q * (L.Hq / L.Hkv), (long long)L.few_rows) * (L.d == 64 ? 2 : 1);
-  return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+  return rows <= 16 ? 16 : 32;
 }
 
 // Key heads (or pairs) whose CTAs form a team: a divisor of them, up to FA_PAGED_TEAM.
@@ -875,14 +875,10 @@ fa_status launch_paged_rows(const PagedLaunch& L, cudaStream_t stream) {
 
 }  // namespace
 
-size_t paged_few_workspace(int rows) { return paged_carve(num_sms(), rows <= 16 ? 16 : (rows <= 32 ? 32 : 64), 128).bytes; }
+size_t paged_few_workspace() { return paged_carve(num_sms(), 32, 128).bytes; }
 
 fa_status launch_paged_few(const PagedLaunch& L, cudaStream_t stream) {
-  switch (paged_rows(L)) {
-    case 16: return launch_paged_rows<16>(L, stream);
-    case 32: return launch_paged_rows<32>(L, stream);
-    default: return launch_paged_rows<64>(L, stream);
-  }
+  return paged_rows(L) == 16 ? launch_paged_rows<16>(L, stream) : launch_paged_rows<32>(L, stream);
 }
 
 }  // namespace fa

@@ -99,4 +99,4 @@ def test_binding_refuses_cpu_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         fa.fa_decode_paged_q8(x, pages, pages, pages, pages, table, lens, 2)
     with pytest.raises(ValueError, match="together"):
-        fa._check_pages(pages, pages, pages, None, table, 1)
+        fa._pages_of(pages, pages, pages, None, table, 1, 0)
