@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       uint32_t g = 0, q_cnt[2] = {0, 0}, p_cnt[2] = {0, 0};
       auto slot_ready = [&](uint32_t i) {
         if (!wait(kv_full + i % L::kStages, (i / L::kStages) & 1)) return false;
-        fence_proxy_async_smem();  // the loaders' writes, before the tensor core reads them
+        if constexpr (!kQ8) fence_proxy_async_smem();  // the loaders' copies, before the tensor core reads them
         tc_fence_after();
         return true;
       };

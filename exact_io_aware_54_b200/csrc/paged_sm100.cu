@@ -51,17 +51,18 @@
 //    the lengths.  A unit that lies in one part is finished there; others leave fp32
 //    partial states, two at most per CTA, that paged_merge_kernel joins in order.  No
 //    atomics: results do not depend on timing.
-//  * Warp roles: 0 MMA issuer, 1 page lookup, 2 K loader, 3 V loader, 4-7 softmax and
-//    epilogue.  The lookup warp turns tiles into rows of the cache, up to eight tiles
+//  * Warp roles: 0 MMA issuer, 1 page lookup, then K loaders, V loaders, and four warps for
+//    softmax and epilogue.  The lookup warp turns tiles into rows of the cache, up to eight tiles
 //    ahead, in a ring that the loaders copy from, and fetches the rows' scale bytes: as the
 //    aligned words that hold them (asynchronous copies have no smaller size), cut out by
 //    the softmax.
 //  * Every role is a small loop: one warp of each runs per scheduler, and with the loaders'
 //    loops unrolled (2000 instructions each) two fifths of all stalls were for instructions
 //    not yet fetched (64 requests, 8 key heads: 499 us).
-//  * Few waits: the issue order Q K^T of tile c + 1, then P V of tile c, makes the scores'
-//    barrier of a tile imply that the products of two tiles before have read their
-//    weights, and the weights' barrier that the scores have been read.
+//  * Few waits: the issue order Q K^T of step s + 1, then P V of step s, makes the scores'
+//    barrier of a step imply that the products of two steps before have read their
+//    weights, and the weights' barrier that the scores have been read; the barrier that
+//    frees a tile's slot tells that its P V is in O.
 #include "paged_common.cuh"
 
 namespace fa {
@@ -70,7 +71,12 @@ using namespace paged;
 
 namespace {
 
-constexpr int kThreads = 256;
+// Loader warps, half of them for K.  One warp each takes about 1050 cycles for a tile of 8
+// bit keys, as long as its bytes do; with 32 rows the softmax takes longer and needs the registers.
+template <int N>
+constexpr int kLoaders = N == 16 ? 4 : 2;
+template <int N>
+constexpr int kThreads = (2 + kLoaders<N> + 4) * 32;
 // Exponent offset and threshold of the running maximum, log2 units.  8 bit: weights
 // up to 2^(7 + 1) use e4m3's range (448) and leave the second piece a floor of
 // 2^-10 / 2^7.  bf16: as in the dense forward.
@@ -82,15 +88,22 @@ struct SoftmaxRange {
 
 template <int N, bool kQ8>
 struct PagedLayout {
-  static constexpr int kSlotBytes = kTile * 128 * (kQ8 ? 1 : 2);  // one K or V tile
-  static constexpr int kSlots = kQ8 ? (N == 32 ? 11 : 12) : 6;  // what fits
+  // Tiles of one step of the MMA issuer and the softmax.  A step has fixed costs (a look at
+  // three barriers, commits, a barrier of the softmax group, latencies in a row) of some
+  // 700 cycles, about the time of an 8 bit tile's bytes: two tiles share them.
+  static constexpr int kPer = kQ8 ? 2 : 1;
+  static constexpr int kTileBytes = kTile * 128 * (kQ8 ? 1 : 2);  // a K or V tile
+  // Slots of one tile each, K and V in turn: K's is free as soon as its scores are there.
+  // (K and V in one slot, a wait less, left the loaders too little room: 287 against 250 us.)
+  static constexpr int kSlotBytes = kTileBytes;
+  static constexpr int kSlots = kQ8 ? (N == 16 ? 11 : 10) : 6;    // what fits
   static constexpr int kRowBlock = N * 128;      // one 128-byte column block of the N rows
   static constexpr int kOffQ = kSlots * kSlotBytes;  // two e4m3 pieces, or two 64-dim blocks
-  static constexpr int kOffP = kOffQ + 2 * kRowBlock;  // double buffer of two e4m3 pieces, or of bf16
-  static constexpr int kOffBar = kOffP + 4 * kRowBlock;
-  // kv_full[S], kv_empty[S], q_full, s_full[2], p_full[2], p_done, rows_full[R], rows_empty[R]
+  static constexpr int kOffP = kOffQ + 2 * kRowBlock;  // [2 steps][kPer] of two e4m3 pieces, or of bf16
+  static constexpr int kOffBar = kOffP + 4 * kPer * kRowBlock;
+  // kv_full[S], kv_empty[S], q_full, s_full[2], p_full[2], rows_full[R], rows_empty[R]
   static constexpr int kRing = 8;  // tiles that the page lookup may be ahead
-  static constexpr int kNumBars = 2 * kSlots + 6 + 2 * kRing;
+  static constexpr int kNumBars = 2 * kSlots + 5 + 2 * kRing;
   static constexpr int kOffMisc = kOffBar + ((kNumBars * 8 + 15) & ~15);
   static constexpr int kOffRows = kOffMisc + 64;
   // per row: factor, limit, threshold, reference, rescale, running max, output row; per warp and row: two sums
@@ -102,7 +115,9 @@ struct PagedLayout {
   static constexpr int kSmemBytes = kOffScales + (kQ8 ? kRing * kTile * 16 : 0) + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory of one SM");
   static constexpr int kCols = kQ8 ? 2 * N : N;  // columns of a product: rows, in 8 bits two pieces of each
-  static constexpr uint32_t kTmemCols = (N == 16 ? 64 : 128) * (kQ8 ? 2 : 1);  // S, S, O
+  static constexpr int kColO = 2 * kPer * kCols;  // behind the scores of two steps
+  static constexpr uint32_t kTmemCols = (N == 16 ? 64 : 128) * (kQ8 ? 4 : 1);
+  static_assert(kColO + kCols <= (int)kTmemCols, "scores of two steps and O");
 };
 
 // rows of one tile that belong to one key head
@@ -221,16 +236,15 @@ __device__ __forceinline__ float2 of_e4m3x2(uint32_t q) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)q, __NV_E4M3)));
 }
 
-// Lane i (mod 32) ends with the sum over the warp of everyone's v[i]; v is used up.
+// Lane i < N ends with the sum over the warp of everyone's v[i]; v is used up.
 template <int N>
 __device__ __forceinline__ float warp_sums(float (&v)[N]) {
-  static_assert(N == 16 || N == 32, "one value per lane at most");
+  static_assert(N == 4 || N == 8 || N == 16 || N == 32, "one value per lane at most");
   const uint32_t lane = lane_id();
-  int live = N;
-  if constexpr (N == 16) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
-  }
+  for (int off = 16; off >= N; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
 #pragma unroll
   for (int off = N / 2; off > 0; off >>= 1) {
     const bool up = (lane & off) != 0;
@@ -240,18 +254,23 @@ __device__ __forceinline__ float warp_sums(float (&v)[N]) {
       const float keep = up ? v[i + off] : v[i];
       v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
     }
-    live = off;
   }
-  (void)live;
   return v[0];
 }
 
-template <int N, bool kQ8, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+// kLive: rows of each key head that there can be, 4 or all of the tile's.  (Four query heads
+// to a key head, or one, and a single token: most decoding.  With the other rows' scores
+// left in place the softmax loop is a quarter of its instructions.)
+template <int N, bool kQ8, int D, int kLive>
+__global__ void __launch_bounds__(kThreads<N>, 1)
     paged_kernel(const PagedArgs a) {
   using L = PagedLayout<N, kQ8>;
   using R = SoftmaxRange<kQ8>;
   constexpr int kHeadRows = head_rows<N, D>();
+  constexpr int kHeads = D == 64 ? 2 : 1;   // key heads side by side
+  constexpr int kRows = kHeads * kLive;     // rows that the softmax looks at
+  // column (row of the tile) of the n-th of them
+  auto col = [](int n) constexpr { return n / kLive * kHeadRows + n % kLive; };
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
@@ -260,8 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = bars + 2 * L::kSlots;
   uint64_t* s_full = q_full + 1;
   uint64_t* p_full = q_full + 3;
-  uint64_t* p_done = q_full + 5;
-  uint64_t* rows_full = q_full + 6;
+  uint64_t* rows_full = q_full + 5;
   uint64_t* rows_empty = rows_full + L::kRing;
   uint32_t* ring_rows = reinterpret_cast<uint32_t*>(smem + L::kOffRing);
   volatile int* ring_tile = reinterpret_cast<volatile int*>(smem + L::kOffTile);
@@ -273,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(sizeof(Work) <= 48, "the stretch fits its place");
   const uint32_t warp = warp_id(), lane = lane_id();
 
-  if (warp == 4) {
+  if (warp == 2) {
     const Work w = find_work<N, D>(a);
     if (lane == 0) {
       *work = w;
@@ -282,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(kv_full + s, 32);  // the copying lanes
+      mbar_init(kv_full + s, kLoaders<N> / 2);  // the warps that share a tile
       mbar_init(kv_empty + s, 1);
     }
     mbar_init(q_full, 4);
@@ -290,10 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
     }
-    mbar_init(p_done, 1);
     for (int i = 0; i < L::kRing; ++i) {
       mbar_init(rows_full + i, kQ8 ? 33 : 1);  // the lookup warp, in 8 bits also its lanes' scale copies
-      mbar_init(rows_empty + i, kQ8 ? 6 : 2);  // both loaders; the softmax warps, which need a row's place for its scales
+      mbar_init(rows_empty + i, kLoaders<N> + (kQ8 ? 4 : 0));  // both loaders; the softmax warps, which need a row's place for its scales
     }
     *abort_flag = 0;
     *group_dead = 0;
@@ -324,15 +341,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     });
     if (!ok && lane == 0) give_up();
-  } else if (warp == 2 || warp == 3) {
+  } else if (warp >= 2 && warp < 2 + kLoaders<N>) {
     // -------------------------------------------------------------------- K and V loaders
-    const bool is_v = warp == 3;
+    constexpr int kParts = kLoaders<N> / 2;  // warps that share a tile
+    const bool is_v = warp >= 2 + kParts;
+    const int part = (warp - 2) % kParts;
     const uint32_t row_bytes = (uint32_t)a.Hkv * D * (kQ8 ? 1 : 2);
     const int chunk = lane & 7, sub = lane >> 3;  // 16-byte chunk of a 128-byte row, key of four
     const uint32_t to0 = sub * 128 + ((chunk ^ sub) << 4), to1 = (sub + 4) * 128 + ((chunk ^ (sub + 4)) << 4);
     const uint32_t ring = smem_u32(ring_rows);
     bool ok = true;
-    for (uint32_t c = 0;; ++c) {
+    uint32_t c = 0;
+    // A tile is handed over once its copies have landed and been made visible to the tensor
+    // core, kLag tiles after they were issued.  (The fence costs the MMA issuer more than
+    // it costs here.)  The ring is long enough for the products never to need a tile
+    // that is held back by a full ring: K of tile c waits for the slot of K or V kSlots / 2
+    // tiles before, whose product needs K of no later tile than c - kLag - 1.
+    constexpr uint32_t kLag = kQ8 ? 2 : 1;
+    auto hand_over = [&](uint32_t x) {
+      fence_proxy_async_smem();
+      mbar_arrive_warp(kv_full + (2 * x + is_v) % L::kSlots);
+    };
+    for (;; ++c) {
       const uint32_t at = c % L::kRing, g = 2 * c + is_v, slot = g % L::kSlots;
       ok = warp_wait(rows_full + at, (c / L::kRing) & 1, a.timeout_ns, abort_flag);
       if (!ok) break;
@@ -343,11 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a pair of 64-dim heads whose second is past the last has no bytes for it
       const bool lone = D == 64 && 2 * hg + 1 >= a.Hkv;
       const uint8_t* src = (is_v ? a.v_pages : a.k_pages) + hg * (kQ8 ? 128 : 256) + chunk * 16;
-      uint32_t dst = smem_u32(smem + slot * L::kSlotBytes);
-      uint32_t rows = ring + (at * kTile + sub) * 4;
+      uint32_t dst = smem_u32(smem + slot * L::kSlotBytes) + part * (128 / kParts) * 128;
+      uint32_t rows = ring + (at * kTile + part * (128 / kParts) + sub) * 4;
       const bool mine = !(kQ8 && lone && chunk >= 4);
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i, dst += 4096, rows += 128) {
+      for (int i = 0; i < 4 / kParts; ++i, dst += 4096, rows += 128) {
         uint32_t rw[8];  // of keys 32 i + 4 j + sub
 #pragma unroll
         for (int j = 0; j < 8; ++j) rw[j] = ld_shared_u32(rows + 16 * j);
@@ -361,12 +391,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mbar_arrive_warp(rows_empty + at);
-      cp_async_arrive(kv_full + slot);
+      cp_async_commit();
+      cp_async_wait<kLag>();
+      if (c >= kLag) hand_over(c - kLag);
     }
-    if (!ok) {
-      if (lane == 0) give_up();
-      cp_async_wait_all();  // copies already issued land before the CTA retires
-    }
+    cp_async_wait_all();  // (also before the CTA retires after a wait that gave up)
+    if (ok)
+      for (uint32_t x = c > kLag ? c - kLag : 0; x < c; ++x) hand_over(x);
+    else if (lane == 0)
+      give_up();
   } else if (warp == 0) {
     // -------------------------------------------------------------------- MMA issuer
     if (lane == 0) {
@@ -378,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const SDesc q_desc = sdesc_make(base + L::kOffQ, 16, 1024);
       const SDesc p_desc = sdesc_make_mn_plain(base + L::kOffP, 128, kTile * 16);  // rows along N: MN-major
       constexpr uint32_t kSlot16 = L::kSlotBytes / 16, kBlock16 = L::kRowBlock / 16;
-      const uint32_t tO = tmem + 2 * L::kCols;
+      const uint32_t tO = tmem + L::kColO;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (ok && !thread_wait(bar, parity, a.timeout_ns, abort_flag)) {
@@ -394,50 +427,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           umma_ss(d, x, y, idesc, accumulate ? 1u : 0u);
       };
-      uint32_t c = 0, piece = 0;  // tiles and pieces so far
-      auto pv = [&](uint32_t x, bool accumulate) {
-        const uint32_t slot = (2 * x + 1) % L::kSlots;
+      uint32_t c = 0, st = 0, piece = 0;  // tiles, steps and pieces so far
+      // P V of step x, tiles c0 ..; its commits free the tiles' slots, and tell the softmax that O is up to date
+      auto pv = [&](uint32_t x, uint32_t c0, int n, bool accumulate) {
         if (!wait(p_full + (x & 1), (x >> 1) & 1)) return;
-        if (!wait(kv_full + slot, ((2 * x + 1) / L::kSlots) & 1)) return;
-        fence_proxy_async_smem();  // the loaders' copies, before the tensor core reads them
         tc_fence_after();
-        const SDesc v = SDesc{v_desc.lo + slot * kSlot16, v_desc.hi};
-        const SDesc pd = SDesc{p_desc.lo + (x & 1) * 2 * kBlock16, p_desc.hi};
-        // keys 32 i .. or 16 i ..
 #pragma unroll
-        for (int i = 0; i < (kQ8 ? 4 : 8); ++i)
-          step(tO, sdesc_at(v, i * (kQ8 ? 256 : 128)), sdesc_at(pd, i * (kQ8 ? 32 : 16)), kIdescO, accumulate || i > 0);
-        umma_commit(p_done);
-        umma_commit(kv_empty + slot);
+        for (int u = 0; u < L::kPer; ++u) {
+          if (u >= n) break;
+          const uint32_t g = 2 * (c0 + u) + 1, slot = g % L::kSlots;
+          if (!wait(kv_full + slot, (g / L::kSlots) & 1)) return;
+          tc_fence_after();
+          const SDesc v = SDesc{v_desc.lo + slot * kSlot16, v_desc.hi};
+          const SDesc pd = SDesc{p_desc.lo + ((x & 1) * L::kPer + u) * 2 * kBlock16, p_desc.hi};
+          // keys 32 i .. or 16 i ..
+#pragma unroll
+          for (int i = 0; i < (kQ8 ? 4 : 8); ++i)
+            step(tO, sdesc_at(v, i * (kQ8 ? 256 : 128)), sdesc_at(pd, i * (kQ8 ? 32 : 16)), kIdescO,
+                 accumulate || u > 0 || i > 0);
+          umma_commit(kv_empty + slot);
+        }
       };
       Piece p;
       while (ok && next_piece<N, D>(a, w, p)) {
         if (!wait(q_full, piece++ & 1)) break;
         tc_fence_after();
-        const int n = p.t1 - p.t0;
-        for (int t = 0; ok && t < n; ++t, ++c) {
-          const uint32_t slot = (2 * c) % L::kSlots;
-          if (!wait(kv_full + slot, ((2 * c) / L::kSlots) & 1)) break;
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const SDesc k = SDesc{k_desc.lo + slot * kSlot16, k_desc.hi};
-          // dims 32 i .. or 16 i .. of two 64-dim blocks
+        const int tiles = p.t1 - p.t0;
+        int last = 0;  // tiles of the step before
+        for (int t = 0; ok && t < tiles; t += L::kPer, ++st) {
+          const int n = min(L::kPer, tiles - t);
 #pragma unroll
-          for (int i = 0; i < (kQ8 ? 4 : 8); ++i)
-            step(tmem + (c & 1) * L::kCols, sdesc_at(k, (i >> 2) * 1024 + (i & 3) * 2),
-                 sdesc_at(q_desc, (i >> 2) * kBlock16 + (i & 3) * 2), kIdescS, i > 0);
-          umma_commit(s_full + (c & 1));
-          umma_commit(kv_empty + slot);
-          if (t > 0) pv(c - 1, t > 1);
+          for (int u = 0; u < L::kPer; ++u) {
+            if (u >= n) break;
+            const uint32_t g = 2 * (c + u), slot = g % L::kSlots;
+            if (!wait(kv_full + slot, (g / L::kSlots) & 1)) break;
+            tc_fence_after();
+            const SDesc k = SDesc{k_desc.lo + slot * kSlot16, k_desc.hi};
+            // dims 32 i .. or 16 i .. of two 64-dim blocks
+#pragma unroll
+            for (int i = 0; i < (kQ8 ? 4 : 8); ++i)
+              step(tmem + ((st & 1) * L::kPer + u) * L::kCols, sdesc_at(k, (i >> 2) * 1024 + (i & 3) * 2),
+                   sdesc_at(q_desc, (i >> 2) * kBlock16 + (i & 3) * 2), kIdescS, i > 0);
+            if (u + 1 < n) umma_commit(kv_empty + slot);
+          }
+          if (!ok) break;
+          umma_commit(s_full + (st & 1));
+          umma_commit(kv_empty + 2 * (c + n - 1) % L::kSlots);
+          if (t > 0) pv(st - 1, c - last, last, t > L::kPer);
+          c += n;
+          last = n;
         }
-        if (ok) pv(c - 1, n > 1);
+        if (ok) pv(st - 1, c - last, last, tiles > L::kPer);
       }
     }
   } else {
     // -------------------------------------------------------------------- softmax and epilogue
     const uint32_t quarter = warp & 3;
     const int r = quarter * 32 + lane;         // key of the tile, then dim of O
-    const int tid = threadIdx.x - 128;         // 0 .. 127
+    const int tid = threadIdx.x - 64 - 32 * kLoaders<N>;  // 0 .. 127
     const uint32_t lanes = (quarter * 32) << 16;
     float* factor = reinterpret_cast<float*>(smem + L::kOffRows);  // of the scores: scale, log2 e, Q's scale
     int* limit = reinterpret_cast<int*>(factor + N);               // first key that the row does not see
@@ -448,17 +495,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* out_row = reinterpret_cast<int*>(factor + 6 * N);  // token * Hq + head, -1: no row
     float* wred = factor + 7 * N;    // [4][N] maxima, then sums
     float* wred2 = wred + 4 * N;
-    uint32_t c = 0;
-    // the N rows of a product, pieces added up
-    auto ld_rows = [&](uint32_t at, float(&x)[N]) {
-      if constexpr (kQ8) {
-        float second[N];
-        tmem_ld_cols2<N>(at, at + N, x, second);
+    uint32_t c = 0, st = 0;  // tiles and steps so far
+    // the rows of a product, pieces added up
+    auto ld_rows = [&](uint32_t at, float(&x)[kRows]) {
+      constexpr int kPieces = kQ8 ? 2 : 1;
+      uint32_t v[kRows * kPieces];
 #pragma unroll
-        for (int n = 0; n < N; ++n) x[n] += second[n];
-      } else {
-        tmem_ld_cols<N>(at, x);
-      }
+      for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) tmem_ld_some<kLive>(at + h * kHeadRows + i * N, v, (i * kHeads + h) * kLive);
+      tmem_ld_done(v);
+#pragma unroll
+      for (int n = 0; n < kRows; ++n)
+        x[n] = kQ8 ? __uint_as_float(v[n]) + __uint_as_float(v[(kPieces - 1) * kRows + n]) : __uint_as_float(v[n]);
     };
     // A wait that gives up does not leave at once: the group's barriers need all four
     // warps, so the warp goes on (waiting no more) to the next place where all leave
@@ -550,211 +599,220 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive_warp(q_full);
       named_bar_sync(1, 128);
-      // rows of each head that there are (the others' columns hold nothing of use)
-      const int live = min(kHeadRows, p.s.nq * a.G - p.rt * kHeadRows);
       // keys that every row of the tile sees: [0, all_see)
       const int first_token = (p.rt * kHeadRows) / a.G;
       const int all_see = a.causal ? max(0, min(p.s.lk, p.s.lk - p.s.nq + first_token + 1)) : p.s.lk;
 
-      float l[N], lr[kQ8 ? 1 : N];
+      float l[kRows], lr[kQ8 ? 1 : kRows];
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
+      for (int n = 0; n < kRows; ++n) {
         l[n] = 0.f;
         if constexpr (!kQ8) lr[n] = 0.f;
       }
 
-      for (int t = 0; t < tiles; ++t, ++c) {
-        const int key = (p.t0 + t) * kTile + r;
-        const int tile_end = (p.t0 + t + 1) * kTile;
-        wait(s_full + (c & 1), (c >> 1) & 1);
+      for (int t = 0; t < tiles; t += L::kPer, ++st) {
+        const int n_tiles = min(L::kPer, tiles - t);
+        const int key0 = (p.t0 + t) * kTile + r;  // this thread's key of the step's first tile
+        wait(s_full + (st & 1), (st >> 1) & 1);
         tc_fence_after();
-        float kf[2] = {1.f, 1.f}, ve[2] = {0.f, 0.f}, vinv[2] = {1.f, 1.f};  // the key's scales, two heads' when d = 64
-        if constexpr (kQ8) {
-          const uint32_t at = c % L::kRing, rw = ring_rows[at * kTile + r];
-          uint4 words;
-          if constexpr (D == 64) {
-            words = reinterpret_cast<const uint4*>(smem + L::kOffScales)[at * kTile + r];
-          } else {
-            const uint2 w2 = reinterpret_cast<const uint2*>(smem + L::kOffScales)[at * kTile + r];
-            words = make_uint4(w2.x, 0, w2.y, 0);
-          }
-          mbar_arrive_warp(rows_empty + at);
-          // byte of the head in its word, and the pair's second head's after it
-          const uint32_t cut = ((rw * (uint32_t)a.Hkv + (D == 64 ? 2 : 1) * p.hg) & 3u) * 8;
-          uint32_t kb = D == 64 ? __funnelshift_r(words.x, words.y, cut) : words.x >> cut;
-          uint32_t vb = D == 64 ? __funnelshift_r(words.z, words.w, cut) : words.z >> cut;
-          if (rw == kNoRow) kb = vb = 0x7F7Fu;  // 2^0
-#pragma unroll
-          for (int h = 0; h < (D == 64 ? 2 : 1); ++h) {
-            kf[h] = __uint_as_float(((kb >> (8 * h)) & 0xFFu) << 23);
-            const int e = (int)((vb >> (8 * h)) & 0xFFu) - 127;
-            ve[h] = (float)e;
-            vinv[h] = __uint_as_float((uint32_t)(127 - e) << 23);
-          }
-        }
-        float y[N];
-        ld_rows(tmem + lanes + (c & 1) * L::kCols, y);
-        const bool masked = tile_end > all_see;
+        float kf[L::kPer][2], ve[L::kPer][2], vinv[L::kPer][2];  // the keys' scales, two heads' when d = 64
+        float y[L::kPer][kRows];
         bool over = !ok;
 #pragma unroll
-        for (int n0 = 0; n0 < N; n0 += 4) {
-          const int h = (D == 64 && n0 >= kHeadRows) ? 1 : 0;
-          if (n0 - h * kHeadRows < live) {
+        for (int u = 0; u < L::kPer; ++u) {
 #pragma unroll
-            for (int n = n0; n < n0 + 4; ++n) {
-              float x = y[n] * factor[n];
-              if constexpr (kQ8) x = fmaf(x, kf[h], ve[h]);
-              if (masked && key >= limit[n]) x = -INFINITY;
-              y[n] = x;
-              over |= x > thresh[n];
+          for (int h = 0; h < 2; ++h) kf[u][h] = vinv[u][h] = 1.f, ve[u][h] = 0.f;
+          if (u >= n_tiles) break;
+          if constexpr (kQ8) {
+            const uint32_t at = (c + u) % L::kRing, rw = ring_rows[at * kTile + r];
+            uint4 words;
+            if constexpr (D == 64) {
+              words = reinterpret_cast<const uint4*>(smem + L::kOffScales)[at * kTile + r];
+            } else {
+              const uint2 w2 = reinterpret_cast<const uint2*>(smem + L::kOffScales)[at * kTile + r];
+              words = make_uint4(w2.x, 0, w2.y, 0);
             }
+            mbar_arrive_warp(rows_empty + at);
+            // byte of the head in its word, and the pair's second head's after it
+            const uint32_t cut = ((rw * (uint32_t)a.Hkv + (D == 64 ? 2 : 1) * p.hg) & 3u) * 8;
+            uint32_t kb = D == 64 ? __funnelshift_r(words.x, words.y, cut) : words.x >> cut;
+            uint32_t vb = D == 64 ? __funnelshift_r(words.z, words.w, cut) : words.z >> cut;
+            if (rw == kNoRow) kb = vb = 0x7F7Fu;  // 2^0
+#pragma unroll
+            for (int h = 0; h < (D == 64 ? 2 : 1); ++h) {
+              kf[u][h] = __uint_as_float(((kb >> (8 * h)) & 0xFFu) << 23);
+              const int e = (int)((vb >> (8 * h)) & 0xFFu) - 127;
+              ve[u][h] = (float)e;
+              vinv[u][h] = __uint_as_float((uint32_t)(127 - e) << 23);
+            }
+          }
+          ld_rows(tmem + lanes + ((st & 1) * L::kPer + u) * L::kCols, y[u]);
+          const int key = key0 + u * kTile;
+          const bool masked = key - r + kTile > all_see;
+#pragma unroll
+          for (int n = 0; n < kRows; ++n) {
+            float x = y[u][n] * factor[col(n)];
+            if constexpr (kQ8) x = fmaf(x, kf[u][n / kLive], ve[u][n / kLive]);
+            if (masked && key >= limit[col(n)]) x = -INFINITY;
+            y[u][n] = x;
+            over |= x > thresh[col(n)];
           }
         }
         if (any_of_group(over)) {
-          // some key exceeds its row's running maximum: the tile's maximum of every row
+          // some key exceeds its row's running maximum: the step's maximum of every row
+          float mine = -INFINITY;
 #pragma unroll
-          for (int n0 = 0; n0 < N; n0 += 32) {
-            float mine = -INFINITY;
+          for (int n = 0; n < kRows; ++n) {
+            float best = y[0][n];
 #pragma unroll
-            for (int i = 0; i < (N < 32 ? N : 32); ++i) {
-              const float m = redux_max(y[n0 + i]);
-              if (lane == (uint32_t)i) mine = m;
-            }
-            if (n0 + (int)lane < N) wred[quarter * N + n0 + lane] = mine;
+            for (int u = 1; u < L::kPer; ++u)
+              if (u < n_tiles) best = fmaxf(best, y[u][n]);
+            const float m = redux_max(best);
+            if (lane == (uint32_t)n) mine = m;
           }
+          if (lane < (uint32_t)kRows) wred[quarter * N + lane] = mine;
           const bool dead = *group_dead != 0;
           named_bar_sync(1, 128);
           if (dead) {
             ok = false;
             break;
           }
-          if (tid < N) {
+          if (tid < kRows) {
             const float m = fmaxf(fmaxf(wred[tid], wred[N + tid]), fmaxf(wred[2 * N + tid], wred[3 * N + tid]));
-            const float old = top[tid];
+            const int x = col(tid);
+            const float old = top[x];
             float al = 1.f;
-            if (m > thresh[tid]) {
+            if (m > thresh[x]) {
               al = old == -INFINITY ? 0.f : ex2(old - m);
-              top[tid] = m;
-              thresh[tid] = m + R::kThreshold;
-              ref[tid] = m - R::kOffset;
+              top[x] = m;
+              thresh[x] = m + R::kThreshold;
+              ref[x] = m - R::kOffset;
             }
-            alpha[tid] = al;
+            alpha[x] = al;
           }
           named_bar_sync(1, 128);
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            l[n] *= alpha[n];
-            if constexpr (!kQ8) lr[n] *= alpha[n];
+          for (int n = 0; n < kRows; ++n) {
+            l[n] *= alpha[col(n)];
+            if constexpr (!kQ8) lr[n] *= alpha[col(n)];
           }
           if (t > 0) {  // O holds earlier tiles: rescale it once the last product is in
-            wait(p_done, (c - 1) & 1);
+            wait(kv_empty + (2 * c - 1) % L::kSlots, ((2 * c - 1) / L::kSlots) & 1);
             tc_fence_after();
+            // columns past the rows there are get whatever alpha holds; they are never read
             uint32_t o[16];
 #pragma unroll 1
             for (int n0 = 0; n0 < L::kCols; n0 += 16) {
-              tmem_ld16(tmem + lanes + 2 * L::kCols + n0, o);
+              tmem_ld16(tmem + lanes + L::kColO + n0, o);
               tmem_ld_wait16(o);
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[n0 % N + i]);
-              tmem_st16(tmem + lanes + 2 * L::kCols + n0, o);
+              tmem_st16(tmem + lanes + L::kColO + n0, o);
             }
             tmem_st_wait();
           }
         }
-        // weights, into the buffer that the product of two tiles ago has read
-        // 16 bytes of rows at a time for this key; rows past the chunk's last are left out
-        const uint32_t pbuf = smem_u32(smem + L::kOffP) + (c & 1) * 2 * L::kRowBlock + r * 16;
+        // weights, into the buffer that the product of two steps ago has read: 16 bytes of
+        // rows at a time for a key; rows past the chunk's last are left out
         constexpr int kGroup = kQ8 ? 16 : 8;
 #pragma unroll
-        for (int n0 = 0; n0 < N; n0 += kGroup) {
-          uint32_t p1[4] = {0, 0, 0, 0}, p2[4] = {0, 0, 0, 0};
+        for (int u = 0; u < L::kPer; ++u) {
+          if (u >= n_tiles) break;
+          const uint32_t pbuf = smem_u32(smem + L::kOffP) + ((st & 1) * L::kPer + u) * 2 * L::kRowBlock + r * 16;
+          // a word of four e4m3 codes, or two words of two bf16 values, for four rows
+          uint32_t p1[N / kGroup][4], p2[N / kGroup][4];
 #pragma unroll
-          for (int i = 0; i < kGroup; i += 4) {
-            const int n = n0 + i;
-            const int h = (D == 64 && n >= kHeadRows) ? 1 : 0;
-            if (n - h * kHeadRows < live) {
-              float pw[4];
+          for (int i = 0; i < N / kGroup; ++i)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                pw[j] = ex2(y[n + j] - ref[n + j]);
-                l[n + j] = fmaf(pw[j], vinv[h], l[n + j]);
-              }
-              if constexpr (kQ8) {
-                const uint32_t lo = to_e4m3x2(pw[0], pw[1]), hi = to_e4m3x2(pw[2], pw[3]);
-                const float2 bl = of_e4m3x2(lo), bh = of_e4m3x2(hi);
-                p1[i / 4] = lo | (hi << 16);
-                p2[i / 4] = to_e4m3x2(pw[0] - bl.x, pw[1] - bl.y) | (to_e4m3x2(pw[2] - bh.x, pw[3] - bh.y) << 16);
-              } else {
+            for (int j = 0; j < 4; ++j) p1[i][j] = p2[i][j] = 0;
 #pragma unroll
-                for (int j = 0; j < 4; j += 2) {
-                  const uint32_t k2 = pack_bf16x2(pw[j], pw[j + 1]);
-                  p1[(i + j) / 2] = k2;
-                  lr[n + j] += __uint_as_float(k2 << 16);
-                  lr[n + j + 1] += __uint_as_float(k2 & 0xFFFF0000u);
-                }
+          for (int n = 0; n < kRows; n += 4) {
+            const int h = n / kLive, x = col(n);
+            float pw[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              pw[j] = ex2(y[u][n + j] - ref[x + j]);
+              l[n + j] = fmaf(pw[j], vinv[u][h], l[n + j]);
+            }
+            if constexpr (kQ8) {
+              const uint32_t lo = to_e4m3x2(pw[0], pw[1]), hi = to_e4m3x2(pw[2], pw[3]);
+              const float2 bl = of_e4m3x2(lo), bh = of_e4m3x2(hi);
+              p1[x / 16][x % 16 / 4] = lo | (hi << 16);
+              p2[x / 16][x % 16 / 4] = to_e4m3x2(pw[0] - bl.x, pw[1] - bl.y) | (to_e4m3x2(pw[2] - bh.x, pw[3] - bh.y) << 16);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; j += 2) {
+                const uint32_t k2 = pack_bf16x2(pw[j], pw[j + 1]);
+                p1[x / 8][(x % 8 + j) / 2] = k2;
+                lr[n + j] += __uint_as_float(k2 << 16);
+                lr[n + j + 1] += __uint_as_float(k2 & 0xFFFF0000u);
               }
             }
           }
-          const uint32_t at = pbuf + (n0 / kGroup) * kTile * 16;
-          st_shared_v4(at, p1[0], p1[1], p1[2], p1[3]);
-          if constexpr (kQ8) st_shared_v4(at + L::kRowBlock, p2[0], p2[1], p2[2], p2[3]);
+#pragma unroll
+          for (int i = 0; i < N / kGroup; ++i) {
+            const uint32_t at = pbuf + i * kTile * 16;
+            st_shared_v4(at, p1[i][0], p1[i][1], p1[i][2], p1[i][3]);
+            if constexpr (kQ8) st_shared_v4(at + L::kRowBlock, p2[i][0], p2[i][1], p2[i][2], p2[i][3]);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive_warp(p_full + (c & 1));
+        mbar_arrive_warp(p_full + (st & 1));
+        c += n_tiles;
       }
       // ---- epilogue: all products of the piece are in (a group that broke off has ok =
       // false in every warp and leaves here)
-      if (ok) wait(p_done, (c - 1) & 1);
+      if (ok) wait(kv_empty + (2 * c - 1) % L::kSlots, ((2 * c - 1) / L::kSlots) & 1);
       if (any_of_group(!ok)) break;
       tc_fence_after();
-      constexpr int kSum = N < 32 ? N : 32;
+      {
+        float v[kRows];
 #pragma unroll
-      for (int n0 = 0; n0 < N; n0 += 32) {
-        float v1[kSum], v2[kSum];
-#pragma unroll
-        for (int i = 0; i < kSum; ++i) {
-          v1[i] = l[n0 + i];
-          if constexpr (!kQ8) v2[i] = lr[n0 + i];
-        }
-        const float s1 = warp_sums<kSum>(v1);
+        for (int n = 0; n < kRows; ++n) v[n] = l[n];
+        const float s1 = warp_sums<kRows>(v);
         float s2 = s1;
-        if constexpr (!kQ8) s2 = warp_sums<kSum>(v2);
-        if ((int)lane < kSum) {
-          wred[quarter * N + n0 + lane] = s1;
-          wred2[quarter * N + n0 + lane] = s2;
+        if constexpr (!kQ8) {
+#pragma unroll
+          for (int n = 0; n < kRows; ++n) v[n] = lr[n];
+          s2 = warp_sums<kRows>(v);
+        }
+        if (lane < (uint32_t)kRows) {
+          wred[quarter * N + lane] = s1;
+          wred2[quarter * N + lane] = s2;
         }
       }
       named_bar_sync(1, 128);
-      float o[N];
-      ld_rows(tmem + lanes + 2 * L::kCols, o);
+      auto sum_of = [&](const float* x, int n) { return (x[n] + x[N + n]) + (x[2 * N + n] + x[3 * N + n]); };
+      float o[kRows];
+      ld_rows(tmem + lanes + L::kColO, o);
       const bool whole = p.t0 == 0 && p.t1 == p.tiles;
       if (whole) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const float sum = (wred2[n] + wred2[N + n]) + (wred2[2 * N + n] + wred2[3 * N + n]);
+        for (int n = 0; n < kRows; ++n) {
+          const float sum = sum_of(wred2, n);
           const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-          const int row = out_row[n];
-          const bool mine = D == 128 || (n >= kHeadRows) == (r >= 64);
+          const int row = out_row[col(n)];
+          const bool mine = D == 128 || n / kLive == r / 64;  // a pair's head has its half of O^T
           if (row >= 0 && mine) a.o[(size_t)row * D + (D == 64 ? (r & 63) : r)] = __float2bfloat16(o[n] * inv);
         }
-        if (tid < N && out_row[tid] >= 0) {
-          const float sum = (wred[tid] + wred[N + tid]) + (wred[2 * N + tid] + wred[3 * N + tid]);
-          const int token = out_row[tid] / a.Hq, head = out_row[tid] - token * a.Hq;
+        if (tid < kRows && out_row[col(tid)] >= 0) {
+          const float sum = sum_of(wred, tid);
+          const int row = out_row[col(tid)], token = row / a.Hq, head = row - token * a.Hq;
           a.lse[token * a.lse_row + head * a.lse_head] =
-              sum == 0.f ? -INFINITY : (ref[tid] + __log2f(sum)) * 0.69314718055994530942f;
+              sum == 0.f ? -INFINITY : (ref[col(tid)] + __log2f(sum)) * 0.69314718055994530942f;
         }
       } else {
         // slot 0: a piece that goes on with a unit begun before; slot 1: a unit begun here
         const size_t slot = 2 * (size_t)blockIdx.x + (p.t0 == 0 ? 1 : 0);
 #pragma unroll
-        for (int n = 0; n < N; ++n) a.part_o[(slot * N + n) * 128 + r] = o[n];
-        if (tid < N) {
-          a.part_m[slot * N + tid] = ref[tid];
-          a.part_l[slot * N + tid] = (wred[tid] + wred[N + tid]) + (wred[2 * N + tid] + wred[3 * N + tid]);
-          a.part_lr[slot * N + tid] = (wred2[tid] + wred2[N + tid]) + (wred2[2 * N + tid] + wred2[3 * N + tid]);
-          if (p.t0 == 0) a.part_rows[(size_t)blockIdx.x * N + tid] = out_row[tid];
+        for (int n = 0; n < kRows; ++n) a.part_o[(slot * N + col(n)) * 128 + r] = o[n];
+        if (tid < kRows) {
+          a.part_m[slot * N + col(tid)] = ref[col(tid)];
+          a.part_l[slot * N + col(tid)] = sum_of(wred, tid);
+          a.part_lr[slot * N + col(tid)] = sum_of(wred2, tid);
         }
+        if (p.t0 == 0 && tid < N) a.part_rows[(size_t)blockIdx.x * N + tid] = out_row[tid];
         if (p.t0 == 0 && tid == 0) {
           // parts up to the team that has the unit's last tile
           const long long last = w.pos - p.t1 + p.tiles - 1;
@@ -816,13 +874,6 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
   }
 }
 
-// Rows per tile: 16 where that holds all rows of one key head's longest chunk that this
-// kernel takes (two heads' when d = 64), else 32.
-int paged_rows(const PagedLaunch& L) {
-  const long long rows = std::min((long long)L.max_q * (L.Hq / L.Hkv), (long long)L.few_rows) * (L.d == 64 ? 2 : 1);
-  return rows <= 16 ? 16 : 32;
-}
-
 // Key heads (or pairs) whose CTAs form a team: a divisor of them, up to FA_PAGED_TEAM.
 #ifndef FA_PAGED_TEAM
 #define FA_PAGED_TEAM 4
@@ -834,12 +885,12 @@ int team_size(int groups, int ctas) {
   return best;
 }
 
-template <int N, bool kQ8, int D>
+template <int N, bool kQ8, int D, int kLive>
 fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
   using L = PagedLayout<N, kQ8>;
   static PerDeviceOnce attr_once;
   if (!attr_once.run([] {
-        return cudaFuncSetAttribute(paged_kernel<N, kQ8, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(paged_kernel<N, kQ8, D, kLive>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     L::kSmemBytes) == cudaSuccess;
       }))
     return FA_ERR_CUDA;
@@ -854,7 +905,7 @@ fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
   a.max_rows = L0.few_rows;
   c.place(a, L0.workspace);
   prof_before(stream, kKPaged);
-  paged_kernel<N, kQ8, D><<<a.teams * a.team, kThreads, L::kSmemBytes, stream>>>(a);
+  paged_kernel<N, kQ8, D, kLive><<<a.teams * a.team, kThreads<N>, L::kSmemBytes, stream>>>(a);
   cudaError_t err = cudaGetLastError();
   prof_after(stream, kKPaged);
   if (err != cudaSuccess) return FA_ERR_CUDA;
@@ -866,11 +917,13 @@ fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
   return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-template <int N>
-fa_status launch_paged_rows(const PagedLaunch& L, cudaStream_t stream) {
-  if (L.k_scales != nullptr)
-    return L.d == 64 ? launch_paged_impl<N, true, 64>(L, stream) : launch_paged_impl<N, true, 128>(L, stream);
-  return L.d == 64 ? launch_paged_impl<N, false, 64>(L, stream) : launch_paged_impl<N, false, 128>(L, stream);
+template <bool kQ8, int D>
+fa_status launch_paged_type(const PagedLaunch& L, cudaStream_t stream) {
+  // rows of one key head's longest chunk that this kernel takes
+  const long long rows = std::min((long long)L.max_q * (L.Hq / L.Hkv), (long long)L.few_rows);
+  if (rows <= 4) return launch_paged_impl<16, kQ8, D, 4>(L, stream);
+  if (rows <= head_rows<16, D>()) return launch_paged_impl<16, kQ8, D, head_rows<16, D>()>(L, stream);
+  return launch_paged_impl<32, kQ8, D, head_rows<32, D>()>(L, stream);
 }
 
 }  // namespace
@@ -878,7 +931,8 @@ fa_status launch_paged_rows(const PagedLaunch& L, cudaStream_t stream) {
 size_t paged_few_workspace() { return paged_carve(num_sms(), 32, 128).bytes; }
 
 fa_status launch_paged_few(const PagedLaunch& L, cudaStream_t stream) {
-  return paged_rows(L) == 16 ? launch_paged_rows<16>(L, stream) : launch_paged_rows<32>(L, stream);
+  if (L.d == 64) return L.k_scales ? launch_paged_type<true, 64>(L, stream) : launch_paged_type<false, 64>(L, stream);
+  return L.k_scales ? launch_paged_type<true, 128>(L, stream) : launch_paged_type<false, 128>(L, stream);
 }
 
 }  // namespace fa

@@ -351,38 +351,36 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
                : "memory");
 }
 
-// N columns of this thread's lane as fp32, loaded and waited for.
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&y)[N]) {
-  static_assert(N % 16 == 0, "whole groups of 16 columns");
-  uint32_t r[N / 16][16];
+// kN (4, 8, 16 or 32) columns of this thread's lane; tmem_ld_done before they are used.
+template <int kN, int kM>
+__device__ __forceinline__ void tmem_ld_some(uint32_t taddr, uint32_t (&r)[kM], int at) {
+  static_assert(kN == 4 || kN == 8 || kN % 16 == 0, "4, 8 or groups of 16 columns");
+  if constexpr (kN == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[at]), "=r"(r[at + 1]), "=r"(r[at + 2]), "=r"(r[at + 3])
+                 : "r"(taddr));
+  } else if constexpr (kN == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[at]), "=r"(r[at + 1]), "=r"(r[at + 2]), "=r"(r[at + 3]), "=r"(r[at + 4]), "=r"(r[at + 5]),
+                   "=r"(r[at + 6]), "=r"(r[at + 7])
+                 : "r"(taddr));
+  } else {
 #pragma unroll
-  for (int i = 0; i < N / 16; ++i) tmem_ld16(taddr + 16 * i, r[i]);
-  tmem_ld_wait16(r[0]);
+    for (int g = 0; g < kN / 16; ++g) {
+      uint32_t x[16];
+      tmem_ld16(taddr + 16 * g, x);
 #pragma unroll
-  for (int i = 1; i < N / 16; ++i) reg_pin16(r[i]);
-#pragma unroll
-  for (int i = 0; i < N; ++i) y[i] = __uint_as_float(r[i / 16][i % 16]);
+      for (int i = 0; i < 16; ++i) r[at + 16 * g + i] = x[i];
+    }
+  }
 }
 
-// N columns each at two places, loaded together and waited for once.
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols2(uint32_t taddr_x, uint32_t taddr_y, float (&x)[N], float (&y)[N]) {
-  static_assert(N % 16 == 0, "whole groups of 16 columns");
-  uint32_t r[N / 8][16];
+// Waits for this thread's tcgen05.ld and pins every use of r after the wait.
+template <int kM>
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[kM]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < N / 16; ++i) {
-    tmem_ld16(taddr_x + 16 * i, r[2 * i]);
-    tmem_ld16(taddr_y + 16 * i, r[2 * i + 1]);
-  }
-  tmem_ld_wait16(r[0]);
-#pragma unroll
-  for (int i = 1; i < N / 8; ++i) reg_pin16(r[i]);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i] = __uint_as_float(r[2 * (i / 16)][i % 16]);
-    y[i] = __uint_as_float(r[2 * (i / 16) + 1][i % 16]);
-  }
+  for (int i = 0; i < kM; ++i) asm volatile("" : "+r"(r[i])::"memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
