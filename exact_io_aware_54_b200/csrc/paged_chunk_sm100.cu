@@ -786,6 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) grid_dependents_launch();
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -796,6 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 // (blockIdx.y of the unit), 32 dims (blockIdx.z), a thread per row.
 template <int D>
 __global__ void __launch_bounds__(128) paged_chunk_merge_kernel(const PagedArgs a) {
+  grid_dependency_wait();  // launched while the attention kernel still runs
   const int cta = blockIdx.x, t = blockIdx.y, r = threadIdx.x;
   const int4 meta = a.meta[cta];
   const int parts = meta.x;
@@ -863,8 +865,7 @@ fa_status launch_chunk_impl(const PagedLaunch& L0, cudaStream_t stream) {
   if (err != cudaSuccess) return FA_ERR_CUDA;
   if (L0.max_k <= kTile) return FA_OK;  // units of one tile are never split
   prof_before(stream, kKPagedChunkMerge);
-  paged_chunk_merge_kernel<D><<<dim3(ctas, 2, D / 32), 128, 0, stream>>>(a);
-  err = cudaGetLastError();
+  err = launch_dependent(paged_chunk_merge_kernel<D>, dim3(ctas, 2, D / 32), 128, stream, a);
   prof_after(stream, kKPagedChunkMerge);
   return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -191,7 +191,28 @@ __device__ __forceinline__ bool look_up_pages(const PagedArgs& a, const PageRing
   return ok;
 }
 
+// Programmatic dependent launch: the second kernel's blocks start when every block of the
+// first has called grid_dependents_launch or ended, and wait for all of its writes.
+__device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ----------------------------------------------------------------------------- host side
+
+// Launches a kernel that begins with grid_dependency_wait behind the stream's last one.
+inline cudaError_t launch_dependent(void (*kernel)(const PagedArgs), dim3 grid, int threads, cudaStream_t stream,
+                                    const PagedArgs& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
+  return err == cudaSuccess ? cudaGetLastError() : err;
+}
 
 inline PagedArgs paged_args(const PagedLaunch& L) {
   PagedArgs a{};

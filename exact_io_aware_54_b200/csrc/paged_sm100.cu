@@ -353,11 +353,10 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
     bool ok = true;
     uint32_t c = 0;
     // A tile is handed over once its copies have landed and been made visible to the tensor
-    // core, kLag tiles after they were issued.  (The fence costs the MMA issuer more than
-    // it costs here.)  The ring is long enough for the products never to need a tile
-    // that is held back by a full ring: K of tile c waits for the slot of K or V kSlots / 2
-    // tiles before, whose product needs K of no later tile than c - kLag - 1.
-    constexpr uint32_t kLag = kQ8 ? 2 : 1;
+    // core: when the next tile's are on their way, or when there is no slot for the next.
+    // (The fence costs the MMA issuer more than it costs here.  64 requests: handed over at
+    // once 316 us, always two tiles late 252, one 241.)
+    bool pending = false;
     auto hand_over = [&](uint32_t x) {
       fence_proxy_async_smem();
       mbar_arrive_warp(kv_full + (2 * x + is_v) % L::kSlots);
@@ -368,7 +367,13 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
       if (!ok) break;
       const int hg = ring_tile[at];
       if (hg < 0) break;
-      ok = warp_wait(kv_empty + slot, ((g / L::kSlots) & 1) ^ 1, a.timeout_ns, abort_flag);
+      const uint32_t free_parity = ((g / L::kSlots) & 1) ^ 1;
+      if (pending && !__all_sync(0xffffffffu, mbar_try_wait(kv_empty + slot, free_parity))) {
+        cp_async_wait_all();
+        hand_over(c - 1);
+        pending = false;
+      }
+      ok = warp_wait(kv_empty + slot, free_parity, a.timeout_ns, abort_flag);
       if (!ok) break;
       // a pair of 64-dim heads whose second is past the last has no bytes for it
       const bool lone = D == 64 && 2 * hg + 1 >= a.Hkv;
@@ -392,14 +397,15 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
       }
       mbar_arrive_warp(rows_empty + at);
       cp_async_commit();
-      cp_async_wait<kLag>();
-      if (c >= kLag) hand_over(c - kLag);
+      if (pending) {
+        cp_async_wait<1>();
+        hand_over(c - 1);
+      }
+      pending = true;
     }
     cp_async_wait_all();  // (also before the CTA retires after a wait that gave up)
-    if (ok)
-      for (uint32_t x = c > kLag ? c - kLag : 0; x < c; ++x) hand_over(x);
-    else if (lane == 0)
-      give_up();
+    if (ok && pending) hand_over(c - 1);
+    if (!ok && lane == 0) give_up();
   } else if (warp == 0) {
     // -------------------------------------------------------------------- MMA issuer
     if (lane == 0) {
@@ -826,6 +832,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) grid_dependents_launch();
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
@@ -838,6 +845,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
 // the i-th team after its.
 template <int N, int D>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
+  grid_dependency_wait();  // launched while the attention kernel still runs
   const int cta = blockIdx.x, parts = a.meta[cta].x;
   if (parts == 0) return;
   const int n = blockIdx.y * 4 + warp_id(), lane = lane_id();
@@ -911,8 +919,7 @@ fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
   if (err != cudaSuccess) return FA_ERR_CUDA;
   if (L0.max_k <= kTile) return FA_OK;  // units of one tile are never split
   prof_before(stream, kKPagedMerge);
-  paged_merge_kernel<N, D><<<dim3(a.teams * a.team, N / 4), 128, 0, stream>>>(a);
-  err = cudaGetLastError();
+  err = launch_dependent(paged_merge_kernel<N, D>, dim3(a.teams * a.team, N / 4), 128, stream, a);
   prof_after(stream, kKPagedMerge);
   return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
