@@ -112,22 +112,40 @@ __global__ void __launch_bounds__(kCacheThreads)
   const int r0 = blockIdx.x * a.rows, nr = min(a.rows, a.total - r0);
   map_rows(a, r0, nr, slot, seq, pos);
   const int per_row = a.H * kLanes, n = nr * per_row;
-  // whole warps run every trip, so that the maximum's shuffles have all lanes
+  // Whole warps run every trip, so that the maximum's shuffles have all lanes.  A trip loads
+  // both tensors' values, and the next trip's before it uses them.
+  auto load = [&](int c, uint4(&x)[4]) {
+    if (c >= n) return;
+    const int r = c / per_row, part = c - r * per_row;  // part: head * kLanes + lane of it
+    const uint4* ks = reinterpret_cast<const uint4*>(k + (r0 + r) * a.k_stride) + 2 * part;
+    const uint4* vs = reinterpret_cast<const uint4*>(v + (r0 + r) * a.v_stride) + 2 * part;
+    x[0] = __ldcs(ks), x[1] = __ldcs(ks + 1), x[2] = __ldcs(vs), x[3] = __ldcs(vs + 1);
+  };
+  uint4 ahead[4] = {};
+  load(threadIdx.x, ahead);
   for (int c0 = threadIdx.x & ~31; c0 < n; c0 += kCacheThreads) {
     const int c = c0 + lane_id();
-    const int r = min(c, n - 1) / per_row, part = min(c, n - 1) - r * per_row;  // part: head * kLanes + lane of it
+    const int r = min(c, n - 1) / per_row, part = min(c, n - 1) - r * per_row;
     const long long s = c < n ? slot[r] : -1;
+    uint4 now[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) now[i] = ahead[i];
+    load(c + kCacheThreads, ahead);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      uint32_t w[8];
-      const uint4* src = reinterpret_cast<const uint4*>((kv ? v : k) + (r0 + r) * (kv ? a.v_stride : a.k_stride)) + 2 * part;
-      const uint4 x = __ldg(src), y = __ldg(src + 1);
-      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+      const uint4 x = now[2 * kv], y = now[2 * kv + 1];
       if constexpr (kQ8) {
+        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max_finite2(m, w[i]);
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
         m = max(m & 0xFFFFu, m >> 16);
+        if (m >= 0x7F80u) {  // an infinity or NaN among them: left out
+          m = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m = max_finite2(m, w[i]);
+          m = max(m & 0xFFFFu, m >> 16);
+        }
 #pragma unroll
         for (int off = 1; off < kLanes; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
         // a = 1.f * 2^(E - 127) <= 1.75 * 2^(8 + e), f the 7 mantissa bits of the bf16 m

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(kv_full + s, 4);  // the loader warps
+      mbar_init(kv_full + s, kQ8 ? 4 : 128);  // a loader warp, or each copying lane
       mbar_init(kv_empty + s, 1);
     }
     for (int i = 0; i < L::kRing; ++i) {
@@ -387,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       uint32_t g = 0, q_cnt[2] = {0, 0}, p_cnt[2] = {0, 0};
       auto slot_ready = [&](uint32_t i) {
         if (!wait(kv_full + i % L::kStages, (i / L::kStages) & 1)) return false;
+        if constexpr (!kQ8) fence_proxy_async_smem();  // the loaders' copies, before the tensor core reads them
         tc_fence_after();
         return true;
       };
@@ -539,22 +540,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         hk = next;
       }
     } else {
-      // a slot is handed over, landed and fenced, when the next one's copies are on their way
-      // or there is no slot for them
-      auto hand_over = [&](uint32_t g) {
-        fence_proxy_async_smem();
-        mbar_arrive_warp(kv_full + g % L::kStages);
-      };
-      bool pending = false;
-      uint32_t g = 0;
+      // Landed copies arrive by themselves, and the MMA issuer fences them: with four slots
+      // a hand-over by the loaders comes too late (8192 tokens of 64-wide heads 311, not 298 us).
 #pragma unroll 1
-      for (; hk >= 0; ++g) {
+      for (uint32_t g = 0; hk >= 0; ++g) {
         const uint8_t* src = (g & 1 ? a.v_pages : a.k_pages) + (size_t)hk * D * 2 + chunk * 16;
-        if (pending && !__all_sync(0xffffffffu, mbar_try_wait(kv_empty + g % L::kStages, ((g / L::kStages) & 1) ^ 1))) {
-          cp_async_wait_all();
-          hand_over(g - 1);
-          pending = false;
-        }
         if (!wait_empty(g)) break;
         const uint32_t tile = tile_of(g) + (chunk >> 3) * L::kBoxBytes;
 #pragma unroll 1
@@ -569,26 +559,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             cp_async16_or_zero(tile + key * 128 + (((chunk & 7) ^ (key & 7)) << 4), src + (uint64_t)(have ? rw[i] : 0u) * row_bytes, have);
           }
         }
-        cp_async_commit();
-        if (pending) {
-          cp_async_wait<1>();
-          hand_over(g - 1);
-        }
-        pending = true;
+        cp_async_arrive(kv_full + g % L::kStages);
         if (g & 1) {
           mbar_arrive_warp(rows_empty + (g >> 1) % L::kRing);
-          // the next tile's rows may not be there yet: what is on its way is not held back for them
-          if (!__all_sync(0xffffffffu, mbar_try_wait(rows_full + ((g >> 1) + 1) % L::kRing, (((g >> 1) + 1) / L::kRing) & 1))) {
-            cp_async_wait_all();
-            hand_over(g);
-            pending = false;
-          }
           hk = head_of((g >> 1) + 1);
         }
-      }
-      if (ok && pending) {
-        cp_async_wait_all();
-        hand_over(g - 1);
       }
     }
     if (!ok && lane == 0) give_up();
