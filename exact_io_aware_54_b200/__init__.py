@@ -20,7 +20,6 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -183,12 +182,12 @@ def paged_workspace(device=None, nbytes: int = 0) -> torch.Tensor:
     workspace.  Calls under stream capture get one of their own from the graph's
     memory, so that graphs share it neither with each other nor with eager calls."""
     index = torch.device(device).index if device is not None else None
-    return _paged_workspace(torch.cuda.current_device() if index is None else index, nbytes)
+    return _paged_workspace(torch.cuda.current_device() if index is None else index, lambda: nbytes)
 
 
-def _paged_workspace(index: int, nbytes: int) -> torch.Tensor:
+def _paged_workspace(index: int, nbytes) -> torch.Tensor:
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=torch.device("cuda", index))
+        ws = torch.empty(max(int(nbytes()), 256), dtype=torch.uint8, device=torch.device("cuda", index))
         ws[:256].zero_()  # the status word; the rest is written before it is read
         return ws
     key = (index, _raw_stream(index))
@@ -619,9 +618,10 @@ def fa_decode_paged(q, k_pages, v_pages, block_table, seqlens_k, max_seqlen_k: i
 _BF16, _FP8, _U8, _I32, _F32 = torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.float32
 
 
-def _on_device(index):
-    """Launches go to the current device: make it the tensors' for the call."""
-    return contextlib.nullcontext() if index == torch.cuda.current_device() else torch.cuda.device(index)
+def _elsewhere(index):
+    """Whether the tensors' device is not the current one, to which launches go: the call is
+    then made again with it current."""
+    return index != torch.cuda.current_device()
 
 
 def _ptr_of(name, t, dtype, shape, index):
@@ -684,7 +684,8 @@ def _pages_of(k_pages, v_pages, k_scales, v_scales, block_table, B, index):
     return shape, most, kp, vp, ks, vs, _ptr_of("block_table", block_table, _I32, (B, most), index)
 
 
-def _paged_ws_of(ws, index, nbytes):
+def _paged_ws_of(ws, index, nbytes=lambda: 256):
+    """Pointer and size of the workspace; nbytes() is what the call needs of one of its own."""
     if ws is None:
         ws = _paged_workspace(index, nbytes)
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != index or not ws.is_contiguous():
@@ -699,8 +700,11 @@ def fa_cache_write(k, v, k_pages, v_pages, cu_seqlens, block_table, seqlens_k, k
     last positions, seqlens_k[b] - n_b .. seqlens_k[b] - 1.  Pages bf16, or
     torch.float8_e4m3fn with scale bytes k_scales, v_scales [num_pages, page_size, H]
     (uint8): a row's slice of one head stands for codes * 2^(byte - 127)."""
-    lib = load()
     index = _device_of("cu_seqlens", cu_seqlens, 1)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return fa_cache_write(k, v, k_pages, v_pages, cu_seqlens, block_table, seqlens_k, k_scales, v_scales, ws)
+    lib = _lib or load()
     B = cu_seqlens.shape[0] - 1
     (P, page, H, d), most, kp, vp, ks, vs, table = _pages_of(k_pages, v_pages, k_scales, v_scales, block_table, B, index)
     total = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
@@ -708,10 +712,9 @@ def fa_cache_write(k, v, k_pages, v_pages, cu_seqlens, block_table, seqlens_k, k
     vr, v_stride = _rows_of("v", v, total, H, d, index)
     cu = _ptr_of("cu_seqlens", cu_seqlens, _I32, (B + 1,), index)
     lens = _ptr_of("seqlens_k", seqlens_k, _I32, (B,), index)
-    with _on_device(index):
-        wp, wn = _paged_ws_of(ws, index, 256)
-        st = lib.fa_cache_write(kr, vr, k_stride, v_stride, cu, table, lens, kp, vp, ks, vs, B, H, total, P, page, most,
-                                d, wp, wn, _raw_stream(index))
+    wp, wn = _paged_ws_of(ws, index)
+    st = lib.fa_cache_write(kr, vr, k_stride, v_stride, cu, table, lens, kp, vp, ks, vs, B, H, total, P, page, most, d,
+                            wp, wn, _raw_stream(index))
     _raise("fa_cache_write", st)
 
 
@@ -720,8 +723,11 @@ def fa_cache_read(k_pages, v_pages, cu_seqlens_k, block_table, total_k: int, k_s
     """Read sequences back from a paged cache: keys 0 .. n_b - 1 of sequence b, n_b =
     cu_seqlens_k[b+1] - cu_seqlens_k[b], into rows cu_seqlens_k[b] .. of (k, v)
     [total_k, H, d] bf16, exactly.  Rows that belong to no sequence are left alone."""
-    lib = load()
     index = _device_of("cu_seqlens_k", cu_seqlens_k, 1)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return fa_cache_read(k_pages, v_pages, cu_seqlens_k, block_table, total_k, k_scales, v_scales, out_k, out_v, ws)
+    lib = _lib or load()
     B, total_k = cu_seqlens_k.shape[0] - 1, int(total_k)
     (P, page, H, d), most, kp, vp, ks, vs, table = _pages_of(k_pages, v_pages, k_scales, v_scales, block_table, B, index)
     shape = (total_k, H, d)
@@ -729,10 +735,8 @@ def fa_cache_read(k_pages, v_pages, cu_seqlens_k, block_table, total_k: int, k_s
     out_v = k_pages.new_empty(shape, dtype=_BF16) if out_v is None else out_v
     ok, ov = _ptr_of("out_k", out_k, _BF16, shape, index), _ptr_of("out_v", out_v, _BF16, shape, index)
     cu = _ptr_of("cu_seqlens_k", cu_seqlens_k, _I32, (B + 1,), index)
-    with _on_device(index):
-        wp, wn = _paged_ws_of(ws, index, 256)
-        st = lib.fa_cache_read(kp, vp, ks, vs, cu, table, ok, ov, B, H, total_k, P, page, most, d, wp, wn,
-                               _raw_stream(index))
+    wp, wn = _paged_ws_of(ws, index)
+    st = lib.fa_cache_read(kp, vp, ks, vs, cu, table, ok, ov, B, H, total_k, P, page, most, d, wp, wn, _raw_stream(index))
     _raise("fa_cache_read", st)
     return out_k, out_v
 
@@ -745,8 +749,12 @@ def fa_fwd_paged(q, k_pages, v_pages, cu_seqlens_q, block_table, seqlens_k, max_
     pages [num_pages, page_size, Hkv, d], bf16 or 8 bit with scales (fa_cache_write);
     query head h reads key head h // (Hq / Hkv).  Returns (o [total_q, Hq, d] bf16,
     lse [Hq, total_q] fp32)."""
-    lib = load()
     index = _device_of("q", q, 3)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return fa_fwd_paged(q, k_pages, v_pages, cu_seqlens_q, block_table, seqlens_k, max_seqlen_q, max_seqlen_k,
+                                causal, softmax_scale, k_scales, v_scales, out, lse, ws)
+    lib = _lib or load()
     total_q, Hq, d = q.shape
     if not isinstance(cu_seqlens_q, torch.Tensor) or cu_seqlens_q.dim() != 1:
         raise ValueError("cu_seqlens_q must be [B+1]")
@@ -762,10 +770,9 @@ def fa_fwd_paged(q, k_pages, v_pages, cu_seqlens_q, block_table, seqlens_k, max_
     op = _ptr_of("out", out, _BF16, (total_q, Hq, d), index)
     lp = _ptr_of("lse", lse, _F32, (Hq, total_q), index)
     max_q, max_k = int(max_seqlen_q), int(max_seqlen_k)
-    with _on_device(index):
-        wp, wn = _paged_ws_of(ws, index, lib.fa_paged_workspace_size(B, Hq, Hkv, max_q, max_k, d))
-        st = lib.fa_fwd_paged(qp, q_stride, kp, vp, ks, vs, cu, table, lens, op, lp, B, Hq, Hkv, total_q, P, page, most,
-                              max_q, max_k, d, int(bool(causal)), _scale(softmax_scale), wp, wn, _raw_stream(index))
+    wp, wn = _paged_ws_of(ws, index, lambda: lib.fa_paged_workspace_size(B, Hq, Hkv, max_q, max_k, d))
+    st = lib.fa_fwd_paged(qp, q_stride, kp, vp, ks, vs, cu, table, lens, op, lp, B, Hq, Hkv, total_q, P, page, most,
+                          max_q, max_k, d, int(bool(causal)), _scale(softmax_scale), wp, wn, _raw_stream(index))
     _raise("fa_fwd_paged", st)
     return out, lse
 
@@ -776,8 +783,12 @@ def fa_decode_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq
     [num_pages, page_size, Hkv, d] torch.float8_e4m3fn with scale bytes [num_pages,
     page_size, Hkv] (fa_cache_write); block_table int32 [B, max_pages_per_seq];
     seqlens_k int32 [B].  Returns (o [B, Hq, d] bf16, lse [B, Hq] fp32)."""
-    lib = load()
     index = _device_of("q", q, 3)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return fa_decode_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, max_seqlen_k,
+                                      softmax_scale, out, lse, ws)
+    lib = _lib or load()
     shape = q.shape
     B, Hq, d = shape
     qp = _ptr_of("q", q, _BF16, shape, index)
@@ -787,14 +798,13 @@ def fa_decode_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq
     if dk != d:
         raise ValueError(f"the pages' head dimension is {dk}, q's is {d}")
     lens = _ptr_of("seqlens_k", seqlens_k, _I32, (B,), index)
-    out = q.new_empty(shape) if out is None else out
+    out = torch.empty_like(q) if out is None else out
     lse = q.new_empty((B, Hq), dtype=_F32) if lse is None else lse
     op, lp = _ptr_of("out", out, _BF16, shape, index), _ptr_of("lse", lse, _F32, (B, Hq), index)
     max_k = int(max_seqlen_k)
-    with _on_device(index):
-        wp, wn = _paged_ws_of(ws, index, lib.fa_paged_workspace_size(B, Hq, Hkv, 1, max_k, d))
-        st = lib.fa_decode_paged_q8(qp, kp, vp, ks, vs, table, lens, B, Hq, Hkv, P, page, most, max_k, d,
-                                    _scale(softmax_scale), op, lp, wp, wn, _raw_stream(index))
+    wp, wn = _paged_ws_of(ws, index, lambda: lib.fa_paged_workspace_size(B, Hq, Hkv, 1, max_k, d))
+    st = lib.fa_decode_paged_q8(qp, kp, vp, ks, vs, table, lens, B, Hq, Hkv, P, page, most, max_k, d,
+                                _scale(softmax_scale), op, lp, wp, wn, _raw_stream(index))
     _raise("fa_decode_paged_q8", st)
     return out, lse
 

@@ -269,7 +269,8 @@ __device__ __forceinline__ void issue_pv_half(uint32_t o_tmem, uint32_t p_tmem, 
 // (bits 8-15 and 24-31) and f = 2^(e + 60) twice.  A code's 7 magnitude bits, moved down by
 // 4, are a bf16 number 2^120 too small, subnormal codes included, so one exact
 // multiplication is left: by 2^(e + 120), of which bf16 holds 2^(e + 60) for every e in
-// [-60, 60].  (Products under 2^-126, of rows with a scale under 2^-57, lose bits.)
+// [-60, 60].  (The smallest product, 2^-9 of the lowest scale, is 2^-129: a bf16 subnormal,
+// still exact.)
 __device__ __forceinline__ uint32_t dequantise2(uint32_t t, uint32_t f) {
   const uint32_t x = (t & 0x80008000u) | ((t >> 4) & 0x07F007F0u);
   uint32_t y;

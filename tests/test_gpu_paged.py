@@ -200,6 +200,71 @@ def test_chunk_long_context(q8):
     _chunk(c, 8, [100], 122)
 
 
+@pytest.mark.parametrize("power", [-66, 55])
+@pytest.mark.parametrize("n", [3, 200])
+def test_chunk_scale_ends(n, power):
+    """Values at the ends of the 8 bit format's scales (codes below the normal numbers at
+    the lower end), keys as quiet as that beside them."""
+    c = Cache(125, [n + 70], 2, 128, 16, True)
+    rng = np.random.default_rng(126)
+    for name, shift in (("k", -66 if power < 0 else 0), ("v", power)):
+        x = torch.from_numpy(rng.standard_normal(c.values[name].shape) * 2.0 ** shift).to(torch.bfloat16)
+        codes, scales = paged.quantise(f64(x))
+        c.values[name] = paged.dequantise(codes, scales)
+        c.pages[name] = torch.from_numpy(codes).view(torch.float8_e4m3fn).cuda()
+        c.scales[name] = torch.from_numpy(scales).cuda()
+    _chunk(c, 4, [n], 127)
+
+
+def test_workspace_is_the_streams():
+    """A bad page is recorded where fa_check looks on that stream, and nowhere else."""
+    c = Cache(128, [40], 1, 64, 16, True)
+    q = synth._normal((1, 1, 64), 129).cuda()
+    table = torch.full_like(c.table, -1)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        fa.fa_decode_paged_q8(q, c.pages["k"], c.pages["v"], c.scales["k"], c.scales["v"], table, c.seqlens, 40)
+    torch.cuda.synchronize()
+    _check()
+    with torch.cuda.stream(other):
+        _check(INVALID)
+    ws = torch.zeros(fa.fa_paged_workspace_size(1, 1, 1, 1, 40, 64), dtype=torch.uint8, device="cuda")
+    fa.fa_decode_paged_q8(q, c.pages["k"], c.pages["v"], c.scales["k"], c.scales["v"], table, c.seqlens, 40, ws=ws)
+    assert fa.fa_check(ws) == INVALID
+    _check()
+
+
+def test_binding_refusals():
+    c = Cache(132, [40], 2, 64, 16, True)
+    q = synth._normal((1, 2, 64), 133).cuda()
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    args = dict(k_pages=c.pages["k"], v_pages=c.pages["v"], block_table=c.table, seqlens_k=c.seqlens, max_seqlen_k=40,
+                **c.kw)
+    fwd = dict(q=q, cu_seqlens_q=cu, max_seqlen_q=1)
+    for bad in (dict(q=q.float()), dict(q=q.expand(1, 2, 64).transpose(1, 2)), dict(k_pages=c.pages["k"][:, :, :1]),
+                dict(k_scales=None), dict(k_scales=c.scales["k"].int()), dict(k_scales=c.scales["k"][:1]),
+                dict(block_table=c.table.long()), dict(block_table=c.table[0]), dict(seqlens_k=c.seqlens.cpu()),
+                dict(cu_seqlens_q=cu.long()), dict(cu_seqlens_q=cu[None]), dict(k_pages=c.pages["k"].view(torch.uint8)),
+                dict(out=torch.empty(1, 2, 64, device="cuda")), dict(lse=torch.empty(1, 2, device="cuda")),
+                dict(ws=torch.zeros(1 << 20, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            fa.fa_fwd_paged(**{**args, **fwd, **bad})
+    for bad in (dict(max_seqlen_k=1 << 20), dict(ws=torch.zeros(64, dtype=torch.uint8, device="cuda")), dict(max_seqlen_q=0)):
+        with pytest.raises(fa.FAError):
+            fa.fa_fwd_paged(**{**args, **fwd, **bad})
+    with pytest.raises(ValueError):  # a bf16 cache where the pages are 8 bit
+        fa.fa_fwd_paged(**{**args, **fwd, "k_scales": None, "v_scales": None})
+    with pytest.raises(ValueError):
+        fa.fa_decode_paged_q8(**{**args, "q": q, "k_scales": None})
+    x = synth._normal((1, 2, 64), 134).cuda()
+    write = dict(k=x, v=x, cu_seqlens=cu, **{k: v for k, v in args.items() if k != "max_seqlen_k"})
+    for bad in (dict(k=x.float()), dict(v=x[:, :1]), dict(k=x.cpu()), dict(cu_seqlens=cu[:1]), dict(v_scales=None)):
+        with pytest.raises(ValueError):
+            fa.fa_cache_write(**{**write, **bad})
+    _check()
+
+
 @pytest.mark.parametrize("n", [2, 200])
 def test_chunk_strided_queries(n):
     """q as a slice of a fused projection."""
