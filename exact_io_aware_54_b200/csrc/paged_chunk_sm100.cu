@@ -307,7 +307,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   static_assert(sizeof(Piece) <= L::kPieceBytes, "a piece fits");
   auto piece_at = [&](uint32_t n) { return reinterpret_cast<Piece*>(smem + L::kOffPieces + n % L::kPieces * L::kPieceBytes); };
 
-  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(kv_full + s, kQ8 ? 4 : 128);  // a loader warp, or each copying lane
@@ -336,6 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
+  // up to here the kernel before may still run
+  grid_dependency_wait();
+  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -802,6 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 template <int D>
 __global__ void __launch_bounds__(128) paged_chunk_merge_kernel(const PagedArgs a) {
   grid_dependency_wait();  // launched while the attention kernel still runs
+  grid_dependents_launch();
   const int cta = blockIdx.x, t = blockIdx.y, r = threadIdx.x;
   const int4 meta = a.meta[cta];
   const int parts = meta.x;
@@ -863,13 +866,12 @@ fa_status launch_chunk_impl(const PagedLaunch& L0, cudaStream_t stream) {
   a.min_rows = L0.few_rows + 1;
   a.max_rows = 0x7fffffff;
   prof_before(stream, kKPagedChunk);
-  paged_chunk_kernel<D, kQ8><<<ctas, kThreads, L::kSmemBytes, stream>>>(a);
-  cudaError_t err = cudaGetLastError();
+  cudaError_t err = launch_dependent(paged_chunk_kernel<D, kQ8>, dim3(ctas), kThreads, L::kSmemBytes, stream, a);
   prof_after(stream, kKPagedChunk);
   if (err != cudaSuccess) return FA_ERR_CUDA;
   if (L0.max_k <= kTile) return FA_OK;  // units of one tile are never split
   prof_before(stream, kKPagedChunkMerge);
-  err = launch_dependent(paged_chunk_merge_kernel<D>, dim3(ctas, 2, D / 32), 128, stream, a);
+  err = launch_dependent(paged_chunk_merge_kernel<D>, dim3(ctas, 2, D / 32), 128, 0, stream, a);
   prof_after(stream, kKPagedChunkMerge);
   return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -198,12 +198,14 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 
 // ----------------------------------------------------------------------------- host side
 
-// Launches a kernel that begins with grid_dependency_wait behind the stream's last one.
-inline cudaError_t launch_dependent(void (*kernel)(const PagedArgs), dim3 grid, int threads, cudaStream_t stream,
-                                    const PagedArgs& a) {
+// Launches a kernel that calls grid_dependency_wait before it touches memory, behind the
+// stream's last one, whose end its own start overlaps.
+inline cudaError_t launch_dependent(void (*kernel)(const PagedArgs), dim3 grid, int threads, size_t smem,
+                                    cudaStream_t stream, const PagedArgs& a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

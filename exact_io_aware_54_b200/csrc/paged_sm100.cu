@@ -291,13 +291,6 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
   static_assert(sizeof(Work) <= 48, "the stretch fits its place");
   const uint32_t warp = warp_id(), lane = lane_id();
 
-  if (warp == 2) {
-    const Work w = find_work<N, D>(a);
-    if (lane == 0) {
-      *work = w;
-      a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-    }
-  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kSlots; ++s) {
       mbar_init(kv_full + s, kLoaders<N> / 2);  // the warps that share a tile
@@ -320,6 +313,15 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
   if (warp == 0) {
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
+  }
+  // up to here the kernel before may still run
+  grid_dependency_wait();
+  if (warp == 2) {
+    const Work w = find_work<N, D>(a);
+    if (lane == 0) {
+      *work = w;
+      a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -842,34 +844,54 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
 // Joins the partial states of the unit that begins in attention CTA blockIdx.x (none:
 // nothing to do), a warp per row: with M the largest reference, every part's sums and
 // O count 2^(m - M).  Part 0 is that CTA's slot 1, part i the slot 0 of the same member of
-// the i-th team after its.
+// the i-th team after its.  Latency is all it costs (a few parts, in L2): what does not
+// depend on one another is loaded together.
 template <int N, int D>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
   grid_dependency_wait();  // launched while the attention kernel still runs
-  const int cta = blockIdx.x, parts = a.meta[cta].x;
-  if (parts == 0) return;
-  const int n = blockIdx.y * 4 + warp_id(), lane = lane_id();
-  const int row = a.part_rows[(size_t)cta * N + n];
-  if (row < 0) return;
+  grid_dependents_launch();
+  const int cta = blockIdx.x, n = blockIdx.y * 4 + warp_id(), lane = lane_id();
+  const int parts = a.meta[cta].x, row = a.part_rows[(size_t)cta * N + n];
+  if (parts == 0 || row < 0) return;
   auto at = [&](int i) { return (2 * (size_t)(cta + i * a.team) + (i == 0 ? 1 : 0)) * N + n; };
-  float M = -INFINITY;
-  for (int i = lane; i < parts; i += 32)
-    if (a.part_l[at(i)] != 0.f) M = fmaxf(M, a.part_m[at(i)]);
-  M = redux_max(M);
   constexpr int kPer = D / 32;
   const int d0 = lane * kPer + (D == 64 && n >= N / 2 ? 64 : 0);
-  float acc[kPer], l = 0.f, lr = 0.f;
+  float M = -INFINITY, acc[kPer], l = 0.f, lr = 0.f;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < parts; ++i) {
-    const float pl = a.part_l[at(i)];
-    const float wt = pl == 0.f ? 0.f : ex2(a.part_m[at(i)] - M);
-    l = fmaf(wt, pl, l);
-    lr = fmaf(wt, a.part_lr[at(i)], lr);
-    const float* src = a.part_o + at(i) * 128 + d0;
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    // lane i: the sums of part i0 + i
+    const bool have = i0 + lane < parts;
+    const size_t own = at(have ? i0 + lane : 0);
+    const float pl = have ? a.part_l[own] : 0.f, pm = have ? a.part_m[own] : -INFINITY, plr = have ? a.part_lr[own] : 0.f;
+    const float top = fmaxf(M, redux_max(pl == 0.f ? -INFINITY : pm));
+    const float keep = M == -INFINITY ? 0.f : ex2(M - top);
+    const float wt = pl == 0.f ? 0.f : ex2(pm - top);
+    M = top;
+    l = l * keep + wt * pl;
+    lr = lr * keep + wt * plr;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, src[e], acc[e]);
+    for (int e = 0; e < kPer; ++e) acc[e] *= keep;
+#pragma unroll 8
+    for (int i = 0; i < min(32, parts - i0); ++i) {
+      const float w = __shfl_sync(0xffffffffu, wt, i);
+      const float* src = a.part_o + at(i0 + i) * 128 + d0;
+      float x[kPer];
+      if constexpr (kPer == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        x[0] = v.x, x[1] = v.y;
+      }
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, off);
+    lr += __shfl_xor_sync(0xffffffffu, lr, off);
   }
   const float inv = lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr);
   __nv_bfloat16* out = a.o + (size_t)row * D + lane * kPer;
@@ -913,13 +935,13 @@ fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
   a.max_rows = L0.few_rows;
   c.place(a, L0.workspace);
   prof_before(stream, kKPaged);
-  paged_kernel<N, kQ8, D, kLive><<<a.teams * a.team, kThreads<N>, L::kSmemBytes, stream>>>(a);
-  cudaError_t err = cudaGetLastError();
+  cudaError_t err =
+      launch_dependent(paged_kernel<N, kQ8, D, kLive>, dim3(a.teams * a.team), kThreads<N>, L::kSmemBytes, stream, a);
   prof_after(stream, kKPaged);
   if (err != cudaSuccess) return FA_ERR_CUDA;
   if (L0.max_k <= kTile) return FA_OK;  // units of one tile are never split
   prof_before(stream, kKPagedMerge);
-  err = launch_dependent(paged_merge_kernel<N, D>, dim3(a.teams * a.team, N / 4), 128, stream, a);
+  err = launch_dependent(paged_merge_kernel<N, D>, dim3(a.teams * a.team, N / 4), 128, 0, stream, a);
   prof_after(stream, kKPagedMerge);
   return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
