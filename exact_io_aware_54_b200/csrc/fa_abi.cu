@@ -129,18 +129,6 @@ bool encode_rows_map(CUtensorMap* map, const void* ptr, int rows, int H, int D, 
   return r == CUDA_SUCCESS;
 }
 
-bool encode_matrix_map(CUtensorMap* map, const void* ptr, long long rows, int cols, bool bytes, int box_rows) {
-  EncodeTiledFn fn = get_encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * (bytes ? 1 : 2)};
-  const cuuint32_t box[2] = {bytes ? 128u : 64u, (cuuint32_t)box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr),
-            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 unsigned long long wait_timeout_ns() {
   static unsigned long long v = [] {
     unsigned long long ms = 2000;

@@ -97,10 +97,6 @@ bool encode_bshd_map(CUtensorMap* map, const void* ptr, int B, int N, int H, int
 // box_rows rows, 128-byte swizzled (zeros outside the tensor).
 bool encode_rows_map(CUtensorMap* map, const void* ptr, int rows, int H, int D, int box_rows);
 
-// Map of a row-major [rows, cols] tensor of bytes (bytes = true) or bf16, boxes of 128
-// bytes x box_rows rows, 128-byte swizzled (zeros outside the tensor).
-bool encode_matrix_map(CUtensorMap* map, const void* ptr, long long rows, int cols, bool bytes, int box_rows);
-
 struct FwdLaunch {
   const void* q;
   const void* k;

@@ -33,9 +33,8 @@
 //  * Tiles of the cache come by 16-byte asynchronous copies, a warp for K and one for V,
 //    each row from wherever its page is, so any page size costs the same; rows past the
 //    sequence's end are filled with zeros (stale shared memory could hold NaN, which a
-//    weight of zero does not remove).  TMA boxes cost some 200 cycles each whatever their
-//    size: with pages of 16 keys 16 of them a tile, 3000 cycles where its bytes take 1400
-//    (64 requests, 8 key heads: 516 us).
+//    weight of zero does not remove).  A TMA box costs its issuer some 260 cycles whatever its
+//    size: pages of 16 keys make 16 of a K and V tile, 4200 cycles where its bytes take 1400.
 //  * The running maximum moves only when some key exceeds it by more than a
 //    threshold: a tile costs one barrier that ORs "does any of my scores exceed",
 //    and the reduction across the 128 keys happens only then.  The l sums stay per
@@ -44,9 +43,8 @@
 //    unrounded sum: its weights carry the value scales, so that a key of quiet values
 //    may round to nothing in the product and still count fully in the sum.
 //  * Work split: CTAs come in teams of neighbouring key heads, which read the same keys'
-//    neighbouring bytes at about the same time (a head's slice of a row is 128 bytes in 8
-//    bits: alone, such reads leave most of HBM's rate unused, 64 requests of 8 key heads
-//    675 us).  A (sequence, team's heads, row tile) unit costs ceil(L / 128) tiles; the line
+//    neighbouring bytes at about the same time: a head's slice of a row is only 128 bytes in
+//    8 bits (64 requests of 8 key heads: 262 us without teams, 253 in teams of 2, 4 or 8).  A (sequence, team's heads, row tile) unit costs ceil(L / 128) tiles; the line
 //    of all units' tiles is cut into equal parts, one per team (one CTA per SM), whatever
 //    the lengths.  A unit that lies in one part is finished there; others leave fp32
 //    partial states, two at most per CTA, that paged_merge_kernel joins in order.  No
@@ -58,7 +56,11 @@
 //    the softmax.
 //  * Every role is a small loop: one warp of each runs per scheduler, and with the loaders'
 //    loops unrolled (2000 instructions each) two fifths of all stalls were for instructions
-//    not yet fetched (64 requests, 8 key heads: 499 us).
+//    not yet fetched (64 requests, 8 key heads: 499 us; 272 with small loops over a ring of rows).
+//  * What it measures: 64 requests of 512 to 16384 keys, 32 query and 8 key heads of 128, 8 bit: 223 us, 85% of
+//    the measured copy rate; bound by the softmax and MMA chain of a tile, which then takes
+//    about as long as its bytes.  One sequence of 8192 keys, 32 heads: 25 us for 10 us of
+//    bytes, the rest the two launches, the pipeline's fill and the join.
 //  * Few waits: the issue order Q K^T of step s + 1, then P V of step s, makes the scores'
 //    barrier of a step imply that the products of two steps before have read their
 //    weights, and the weights' barrier that the scores have been read; the barrier that
@@ -72,7 +74,7 @@ using namespace paged;
 namespace {
 
 // Loader warps, half of them for K.  One warp each takes about 1050 cycles for a tile of 8
-// bit keys, as long as its bytes do; with 32 rows the softmax takes longer and needs the registers.
+// bit keys, as long as its bytes do: two are never ahead.  With 32 rows the softmax takes longer and needs the registers.
 template <int N>
 constexpr int kLoaders = N == 16 ? 4 : 2;
 template <int N>
@@ -94,7 +96,7 @@ struct PagedLayout {
   static constexpr int kPer = kQ8 ? 2 : 1;
   static constexpr int kTileBytes = kTile * 128 * (kQ8 ? 1 : 2);  // a K or V tile
   // Slots of one tile each, K and V in turn: K's is free as soon as its scores are there.
-  // (K and V in one slot, a wait less, left the loaders too little room: 287 against 250 us.)
+  // (K and V in one slot, a wait less, left the loaders too little room: 287 against 259 us.)
   static constexpr int kSlotBytes = kTileBytes;
   static constexpr int kSlots = kQ8 ? (N == 16 ? 11 : 10) : 6;    // what fits
   static constexpr int kRowBlock = N * 128;      // one 128-byte column block of the N rows
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
     }
     for (int i = 0; i < L::kRing; ++i) {
       mbar_init(rows_full + i, kQ8 ? 33 : 1);  // the lookup warp, in 8 bits also its lanes' scale copies
-      mbar_init(rows_empty + i, kLoaders<N> + (kQ8 ? 4 : 0));  // both loaders; the softmax warps, which need a row's place for its scales
+      mbar_init(rows_empty + i, kLoaders<N> + (kQ8 ? 4 : 0));  // the loaders, and the softmax warps for the scales' words
     }
     *abort_flag = 0;
     *group_dead = 0;
@@ -904,13 +906,12 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
   }
 }
 
-// Key heads (or pairs) whose CTAs form a team: a divisor of them, up to FA_PAGED_TEAM.
-#ifndef FA_PAGED_TEAM
-#define FA_PAGED_TEAM 4
-#endif
+// Key heads (or pairs) whose CTAs form a team: a divisor of them, up to kMaxTeam, that leaves
+// next to no CTA without a team.
+constexpr int kMaxTeam = 4;
 int team_size(int groups, int ctas) {
   int best = 1;
-  for (int t = 2; t <= std::min({groups, ctas, FA_PAGED_TEAM}); ++t)
+  for (int t = 2; t <= std::min({groups, ctas, kMaxTeam}); ++t)
     if (groups % t == 0 && ctas / t * t >= ctas / best * best * 31 / 32) best = t;
   return best;
 }
