@@ -39,13 +39,17 @@ namespace {
 constexpr int kThreads = 512;
 // registers per thread of the four warpgroups, out of 4 x 128
 template <bool kQ8>
-constexpr uint32_t kRegsIssue = kQ8 ? 64 : 88;
+constexpr uint32_t kRegsIssue = kQ8 ? 72 : 88;
 template <bool kQ8>
-constexpr uint32_t kRegsLoad = kQ8 ? 80 : 56;
+constexpr uint32_t kRegsLoad = kQ8 ? 72 : 56;
 constexpr uint32_t kRegsSoftmax = 184;
 static_assert(kRegsIssue<true> + kRegsLoad<true> + 2 * kRegsSoftmax <= 4 * 128 &&
                   kRegsIssue<false> + kRegsLoad<false> + 2 * kRegsSoftmax <= 4 * 128,
               "register split exceeds the launch budget");
+// Loader warps, up to warp 7.  Converting 8 bit tiles of 128-wide heads is what bounds the
+// kernel, so the two warps beside the MMA issuer and the page lookup help.
+template <int D, bool kQ8>
+constexpr int kLoaders = kQ8 && D == 128 ? 6 : 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kUnitRows = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -313,12 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(kv_full + s, kQ8 ? 4 : 128);  // a loader warp, or each copying lane
+      mbar_init(kv_full + s, kQ8 ? kLoaders<D, kQ8> : 128);  // a loader warp, or each copying lane
       mbar_init(kv_empty + s, 1);
     }
     for (int i = 0; i < L::kRing; ++i) {
       mbar_init(rows_full + i, kQ8 ? 33 : 1);
-      mbar_init(rows_empty + i, 4);
+      mbar_init(rows_empty + i, kLoaders<D, kQ8>);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full + t, 4);
@@ -351,11 +355,128 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     atomicCAS(a.status, 0, kStatusTimeout);
   };
 
-  if (warp < 4) {
+  // ------------------------------------------------------------------ loaders
+  auto load_tiles = [&]() {
+    constexpr int kChunks = D * (kQ8 ? 1 : 2) / 16;  // 16-byte pieces of a cache row's slice
+    constexpr int kKeys = 32 / kChunks;              // keys per step of the warp
+    // steps of the warps past 3, and of 2 and 3 if they load
+    constexpr int kMost = kLoaders<D, kQ8> == 6 ? 24 / kKeys : 32 / kKeys, kFew = kLoaders<D, kQ8> == 6 ? 16 / kKeys : kMost;
+    const int steps = warp < 4 ? kFew : kMost;
+    const uint32_t row_bytes = (uint32_t)a.Hkv * D * (kQ8 ? 1 : 2);
+    const int chunk = lane % kChunks, sub = lane / kChunks, first = kTile - (warp < 4 ? 4 * kMost + (4 - (int)warp) * kFew : (8 - (int)warp) * kMost) * kKeys;
+    const uint32_t ring = smem_u32(ring_rows), words = smem_u32(smem + L::kOffScales);
+    bool ok = true;
+    // head of tile c, -1 after the last; row of key first + i kKeys + sub
+    auto head_of = [&](uint32_t c) {
+      ok = warp_wait(rows_full + c % L::kRing, (c / L::kRing) & 1, a.timeout_ns, abort_flag);
+      return ok ? ring_tile[c % L::kRing] : -1;
+    };
+    auto row_of = [&](uint32_t c, int i) { return ld_shared_u32(ring + ((c % L::kRing) * kTile + first + i * kKeys + sub) * 4); };
+    auto tile_of = [&](uint32_t g) { return smem_u32(smem + L::kOffSlots + (g % L::kStages) * L::kTileBytes); };
+    auto wait_empty = [&](uint32_t g) {
+      ok = warp_wait(kv_empty + g % L::kStages, ((g / L::kStages) & 1) ^ 1, a.timeout_ns, abort_flag);
+      return ok;
+    };
+    int hk = head_of(0);
+    if constexpr (kQ8) {
+      // Slot after slot (K, V of tile 0, K of tile 1, ..).  Each lane's 16 codes of a step
+      // come by an asynchronous copy to a place that only it reads, a slot ahead: no
+      // registers held, and the loop stays at one step's instructions.  (Unrolled over a
+      // slot or more, loads in registers, the loaders and the softmax together outgrew
+      // the instruction cache: 8192 tokens 1190 us.)
+      constexpr int kTogether = 2;  // steps converted side by side (one: 981 us; four: as two)
+      const uint32_t codes = smem_u32(smem + L::kOffCodes) + (first * D) + lane * 16;
+      auto copy = [&](uint32_t g, int head, int i) {
+        const uint32_t row = row_of(g >> 1, i);
+        const uint8_t* src = (g & 1 ? a.v_pages : a.k_pages) + (size_t)head * D + chunk * 16;
+        cp_async16_or_zero(codes + i * 512, src + (uint64_t)(row != kNoRow ? row : 0u) * row_bytes, row != kNoRow);
+      };
+      if (hk >= 0) {
+#pragma unroll 1
+        for (int i = 0; i < steps; ++i) {
+          copy(0, hk, i);
+          cp_async_commit();
+        }
+      }
+#pragma unroll 1
+      for (uint32_t g = 0; hk >= 0; ++g) {
+        const int next = g & 1 ? head_of((g >> 1) + 1) : hk;
+        if (!ok || !wait_empty(g)) break;
+        const uint32_t tile = tile_of(g) + (chunk >> 2) * L::kBoxBytes;
+        const uint32_t word_at = words + (((g >> 1) % L::kRing) * kTile + first + sub) * 8 + (g & 1) * 4;
+#pragma unroll 1
+        for (int i0 = 0; i0 < steps; i0 += kTogether) {
+          uint32_t row[kTogether], word[kTogether];
+          uint4 x[kTogether];
+          if (warp < 4)
+            cp_async_wait<kFew - kTogether>();
+          else
+            cp_async_wait<kMost - kTogether>();
+#pragma unroll
+          for (int j = 0; j < kTogether; ++j) {
+            row[j] = row_of(g >> 1, i0 + j);
+            word[j] = ld_shared_u32(word_at + (i0 + j) * kKeys * 8);
+            ld_shared_v4(codes + (i0 + j) * 512, x[j].x, x[j].y, x[j].z, x[j].w);
+          }
+#pragma unroll
+          for (int j = 0; j < kTogether; ++j) {
+            const int key = first + (i0 + j) * kKeys + sub;
+            const uint32_t cut = ((row[j] * (uint32_t)a.Hkv + hk) & 3u) * 8;
+            // past the sequence's end the codes are zeros, and the word holds anything
+            const uint32_t f = row[j] != kNoRow ? ((((word[j] >> cut) & 0xFFu) + 60u) << 7) * 0x00010001u : 0u;
+            const uint2 w0 = dequantise4(x[j].x, f), w1 = dequantise4(x[j].y, f), w2 = dequantise4(x[j].z, f),
+                        w3 = dequantise4(x[j].w, f);
+            const uint32_t to = tile + key * 128, c2 = 2 * (chunk & 3);  // 16-byte chunks of the bf16 row: c2 and c2 + 1
+            st_shared_v4(to + ((c2 ^ (key & 7)) << 4), w0.x, w0.y, w1.x, w1.y);
+            st_shared_v4(to + (((c2 + 1) ^ (key & 7)) << 4), w2.x, w2.y, w3.x, w3.y);
+          }
+#pragma unroll
+          for (int j = 0; j < kTogether; ++j) {
+            if (next >= 0) copy(g + 1, next, i0 + j);  // (the codes have been read: they were used above)
+            cp_async_commit();
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive_warp(kv_full + g % L::kStages);
+        if (g & 1) mbar_arrive_warp(rows_empty + (g >> 1) % L::kRing);
+        hk = next;
+      }
+    } else {
+      // Landed copies arrive by themselves, and the MMA issuer fences them: with four slots
+      // a hand-over by the loaders comes too late (8192 tokens of 64-wide heads 311, not 298 us).
+#pragma unroll 1
+      for (uint32_t g = 0; hk >= 0; ++g) {
+        const uint8_t* src = (g & 1 ? a.v_pages : a.k_pages) + (size_t)hk * D * 2 + chunk * 16;
+        if (!wait_empty(g)) break;
+        const uint32_t tile = tile_of(g) + (chunk >> 3) * L::kBoxBytes;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kMost; i0 += 8) {
+          uint32_t rw[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) rw[i] = row_of(g >> 1, i0 + i);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int key = first + (i0 + i) * kKeys + sub;
+            const bool have = rw[i] != kNoRow;
+            cp_async16_or_zero(tile + key * 128 + (((chunk & 7) ^ (key & 7)) << 4), src + (uint64_t)(have ? rw[i] : 0u) * row_bytes, have);
+          }
+        }
+        cp_async_arrive(kv_full + g % L::kStages);
+        if (g & 1) {
+          mbar_arrive_warp(rows_empty + (g >> 1) % L::kRing);
+          hk = head_of((g >> 1) + 1);
+        }
+      }
+    }
+    if (!ok && lane == 0) give_up();
+    cp_async_wait_all();
+  };
+
+  if (warp < (kQ8 ? 8 : 4)) {
     regs_dec<kRegsIssue<kQ8>>();
     if (warp == 1) {
       // ------------------------------------------------------------------ page lookup
-      const PageRing ring{ring_rows, ring_tile, smem_u32(smem + L::kOffScales), rows_full, rows_empty};
+      const PageRing ring{ring_rows, ring_tile, smem_u32(smem + L::kOffScales), rows_full, rows_full, rows_empty};
       Work w = find_work(a);
       uint32_t n = 0;
       bool fine = true;
@@ -463,118 +584,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           if (t == 0 || rows > 128) umma_commit(o_done + t);
         mbar_arrive(piece_empty + n % L::kPieces);
       }
+    } else if (kQ8 && warp >= 8 - kLoaders<D, kQ8>) {
+      load_tiles();
     }
-  } else if (warp < 8) {
+  } else if (!kQ8 && warp < 8) {
     regs_dec<kRegsLoad<kQ8>>();
-    // ------------------------------------------------------------------ loaders: keys 32 (warp - 4) .. of every tile
-    constexpr int kChunks = D * (kQ8 ? 1 : 2) / 16;  // 16-byte pieces of a cache row's slice
-    constexpr int kKeys = 32 / kChunks;              // keys per step of the warp
-    constexpr int kSteps = 32 / kKeys;
-    const uint32_t row_bytes = (uint32_t)a.Hkv * D * (kQ8 ? 1 : 2);
-    const int chunk = lane % kChunks, sub = lane / kChunks, first = ((int)warp - 4) * 32;
-    const uint32_t ring = smem_u32(ring_rows), words = smem_u32(smem + L::kOffScales);
-    bool ok = true;
-    // head of tile c, -1 after the last; row of key first + i kKeys + sub
-    auto head_of = [&](uint32_t c) {
-      ok = warp_wait(rows_full + c % L::kRing, (c / L::kRing) & 1, a.timeout_ns, abort_flag);
-      return ok ? ring_tile[c % L::kRing] : -1;
-    };
-    auto row_of = [&](uint32_t c, int i) { return ld_shared_u32(ring + ((c % L::kRing) * kTile + first + i * kKeys + sub) * 4); };
-    auto tile_of = [&](uint32_t g) { return smem_u32(smem + L::kOffSlots + (g % L::kStages) * L::kTileBytes); };
-    auto wait_empty = [&](uint32_t g) {
-      ok = warp_wait(kv_empty + g % L::kStages, ((g / L::kStages) & 1) ^ 1, a.timeout_ns, abort_flag);
-      return ok;
-    };
-    int hk = head_of(0);
-    if constexpr (kQ8) {
-      // Slot after slot (K, V of tile 0, K of tile 1, ..).  Each lane's 16 codes of a step
-      // come by an asynchronous copy to a place that only it reads, a slot ahead: no
-      // registers held, and the loop stays at one step's instructions.  (Unrolled over a
-      // slot or more, loads in registers, the loaders and the softmax together outgrew
-      // the instruction cache: 8192 tokens 1190 us.)
-      constexpr int kTogether = 2;  // steps converted side by side (one: 981 us; four: as two)
-      const uint32_t codes = smem_u32(smem + L::kOffCodes) + (first * D) + lane * 16;
-      auto copy = [&](uint32_t g, int head, int i) {
-        const uint32_t row = row_of(g >> 1, i);
-        const uint8_t* src = (g & 1 ? a.v_pages : a.k_pages) + (size_t)head * D + chunk * 16;
-        cp_async16_or_zero(codes + i * 512, src + (uint64_t)(row != kNoRow ? row : 0u) * row_bytes, row != kNoRow);
-      };
-      if (hk >= 0) {
-#pragma unroll 1
-        for (int i = 0; i < kSteps; ++i) {
-          copy(0, hk, i);
-          cp_async_commit();
-        }
-      }
-#pragma unroll 1
-      for (uint32_t g = 0; hk >= 0; ++g) {
-        const int next = g & 1 ? head_of((g >> 1) + 1) : hk;
-        if (!ok || !wait_empty(g)) break;
-        const uint32_t tile = tile_of(g) + (chunk >> 2) * L::kBoxBytes;
-        const uint32_t word_at = words + (((g >> 1) % L::kRing) * kTile + first + sub) * 8 + (g & 1) * 4;
-#pragma unroll 1
-        for (int i0 = 0; i0 < kSteps; i0 += kTogether) {
-          uint32_t row[kTogether], word[kTogether];
-          uint4 x[kTogether];
-          cp_async_wait<kSteps - kTogether>();
-#pragma unroll
-          for (int j = 0; j < kTogether; ++j) {
-            row[j] = row_of(g >> 1, i0 + j);
-            word[j] = ld_shared_u32(word_at + (i0 + j) * kKeys * 8);
-            ld_shared_v4(codes + (i0 + j) * 512, x[j].x, x[j].y, x[j].z, x[j].w);
-          }
-#pragma unroll
-          for (int j = 0; j < kTogether; ++j) {
-            const int key = first + (i0 + j) * kKeys + sub;
-            const uint32_t cut = ((row[j] * (uint32_t)a.Hkv + hk) & 3u) * 8;
-            // past the sequence's end the codes are zeros, and the word holds anything
-            const uint32_t f = row[j] != kNoRow ? ((((word[j] >> cut) & 0xFFu) + 60u) << 7) * 0x00010001u : 0u;
-            const uint2 w0 = dequantise4(x[j].x, f), w1 = dequantise4(x[j].y, f), w2 = dequantise4(x[j].z, f),
-                        w3 = dequantise4(x[j].w, f);
-            const uint32_t to = tile + key * 128, c2 = 2 * (chunk & 3);  // 16-byte chunks of the bf16 row: c2 and c2 + 1
-            st_shared_v4(to + ((c2 ^ (key & 7)) << 4), w0.x, w0.y, w1.x, w1.y);
-            st_shared_v4(to + (((c2 + 1) ^ (key & 7)) << 4), w2.x, w2.y, w3.x, w3.y);
-          }
-#pragma unroll
-          for (int j = 0; j < kTogether; ++j) {
-            if (next >= 0) copy(g + 1, next, i0 + j);  // (the codes have been read: they were used above)
-            cp_async_commit();
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive_warp(kv_full + g % L::kStages);
-        if (g & 1) mbar_arrive_warp(rows_empty + (g >> 1) % L::kRing);
-        hk = next;
-      }
-    } else {
-      // Landed copies arrive by themselves, and the MMA issuer fences them: with four slots
-      // a hand-over by the loaders comes too late (8192 tokens of 64-wide heads 311, not 298 us).
-#pragma unroll 1
-      for (uint32_t g = 0; hk >= 0; ++g) {
-        const uint8_t* src = (g & 1 ? a.v_pages : a.k_pages) + (size_t)hk * D * 2 + chunk * 16;
-        if (!wait_empty(g)) break;
-        const uint32_t tile = tile_of(g) + (chunk >> 3) * L::kBoxBytes;
-#pragma unroll 1
-        for (int i0 = 0; i0 < kSteps; i0 += 8) {
-          uint32_t rw[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) rw[i] = row_of(g >> 1, i0 + i);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int key = first + (i0 + i) * kKeys + sub;
-            const bool have = rw[i] != kNoRow;
-            cp_async16_or_zero(tile + key * 128 + (((chunk & 7) ^ (key & 7)) << 4), src + (uint64_t)(have ? rw[i] : 0u) * row_bytes, have);
-          }
-        }
-        cp_async_arrive(kv_full + g % L::kStages);
-        if (g & 1) {
-          mbar_arrive_warp(rows_empty + (g >> 1) % L::kRing);
-          hk = head_of((g >> 1) + 1);
-        }
-      }
-    }
-    if (!ok && lane == 0) give_up();
-    cp_async_wait_all();
+    load_tiles();
   } else {
     regs_inc<kRegsSoftmax>();
     // ------------------------------------------------------------------ softmax groups

@@ -110,13 +110,15 @@ __device__ __forceinline__ float redux_max(float x) {
 // pages that hold the tile's keys (kNoRow past the sequence's end), the key head (or pair of
 // heads), -1 after the last tile, and in 8 bits per key the words that hold its K and V
 // scale bytes, one each, or two each (K, K, V, V) when the heads of a pair may lie in
-// different words.  `full` counts
-// one arrival, in 8 bits 33; the readers arrive on `empty`.
+// different words.  Rows and head arrive on `full`, once; the words, which are a trip to
+// memory later, on `scaled`, once a lane.  (The two may be one barrier of 33 arrivals.)
+// The readers arrive on `empty`.
 struct PageRing {
   uint32_t* rows;
   volatile int* tile;
   uint32_t scales;  // shared-memory address
   uint64_t* full;
+  uint64_t* scaled;
   uint64_t* empty;
 };
 
@@ -132,6 +134,7 @@ __device__ __forceinline__ bool look_up_pages(const PagedArgs& a, const PageRing
     const uint32_t at = c % kRing;
     ok = warp_wait(ring.empty + at, ((c / kRing) & 1) ^ 1, a.timeout_ns, abort_flag);
     if (!ok) return;
+    uint32_t row[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int key = key0 + lane + 32 * i;
@@ -140,14 +143,19 @@ __device__ __forceinline__ bool look_up_pages(const PagedArgs& a, const PageRing
         atomicExch(a.status, kStatusBadArg);
         pg = 0;
       }
-      const uint32_t row = (uint32_t)(pg * a.page_size + (key - page_index(a, key) * a.page_size));
-      ring.rows[at * kTile + lane + 32 * i] = key < lk ? row : kNoRow;
-      if constexpr (kQ8) {
-        if (key < lk) {
+      row[i] = key < lk ? (uint32_t)(pg * a.page_size + (key - page_index(a, key) * a.page_size)) : kNoRow;
+      ring.rows[at * kTile + lane + 32 * i] = row[i];
+    }
+    if (lane == 0) ring.tile[at] = head;
+    mbar_arrive_warp(ring.full + at);
+    if constexpr (kQ8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (row[i] != kNoRow) {
           constexpr int kWords = kPair ? 2 : 1;
           // the words that hold the key's scale bytes (never past the arrays' ends)
           const uint32_t to = ring.scales + (at * kTile + lane + 32 * i) * 8 * kWords;
-          const long long o = ((long long)row * a.Hkv + (kPair ? 2 : 1) * head) & ~3LL;
+          const long long o = ((long long)row[i] * a.Hkv + (kPair ? 2 : 1) * head) & ~3LL;
           const int n0 = (int)min(4LL, a.scale_bytes - o), n1 = (int)max(0LL, min(4LL, a.scale_bytes - o - 4));
           cp_async4(to, a.k_scales + o, n0);
           cp_async4(to + 4 * kWords, a.v_scales + o, n0);
@@ -157,10 +165,8 @@ __device__ __forceinline__ bool look_up_pages(const PagedArgs& a, const PageRing
           }
         }
       }
+      cp_async_arrive(ring.scaled + at);
     }
-    if (lane == 0) ring.tile[at] = head;
-    if constexpr (kQ8) cp_async_arrive(ring.full + at);
-    mbar_arrive_warp(ring.full + at);
     ++c;
   };
   int b, head, t0, t1, lk;

@@ -44,8 +44,8 @@
 //    may round to nothing in the product and still count fully in the sum.
 //  * Work split: CTAs come in teams of neighbouring key heads, which read the same keys'
 //    neighbouring bytes at about the same time: a head's slice of a row is only 128 bytes in
-//    8 bits (64 requests of 8 key heads: 262 us without teams, 253 in teams of 2, 4 or 8).  A (sequence, team's heads, row tile) unit costs ceil(L / 128) tiles; the line
-//    of all units' tiles is cut into equal parts, one per team (one CTA per SM), whatever
+//    8 bits (64 requests of 8 key heads: 262 us without teams, 253 in teams of 2, 4 or 8).  A (sequence, team's heads, row tile) unit counts ceil(L / 128) tiles and
+//    kUnitCost for its start and end; the line of all units is cut into equal parts, one per team (one CTA per SM), whatever
 //    the lengths.  A unit that lies in one part is finished there; others leave fp32
 //    partial states, two at most per CTA, that paged_merge_kernel joins in order.  No
 //    atomics: results do not depend on timing.
@@ -59,8 +59,9 @@
 //    not yet fetched (64 requests, 8 key heads: 499 us; 272 with small loops over a ring of rows).
 //  * What it measures: 64 requests of 512 to 16384 keys, 32 query and 8 key heads of 128, 8 bit: 223 us, 85% of
 //    the measured copy rate; bound by the softmax and MMA chain of a tile, which then takes
-//    about as long as its bytes.  One sequence of 8192 keys, 32 heads: 25 us for 10 us of
-//    bytes, the rest the two launches, the pipeline's fill and the join.
+//    about as long as its bytes.  One sequence of 8192 keys, 32 heads: 22.6 us for 10 us of
+//    bytes, the rest the start (four dependent loads: offsets, page, keys, then the first scores:
+//    5.5 us), the epilogue and the join (1 and 3 us).
 //  * Few waits: the issue order Q K^T of step s + 1, then P V of step s, makes the scores'
 //    barrier of a step imply that the products of two steps before have read their
 //    weights, and the weights' barrier that the scores have been read; the barrier that
@@ -103,9 +104,9 @@ struct PagedLayout {
   static constexpr int kOffQ = kSlots * kSlotBytes;  // two e4m3 pieces, or two 64-dim blocks
   static constexpr int kOffP = kOffQ + 2 * kRowBlock;  // [2 steps][kPer] of two e4m3 pieces, or of bf16
   static constexpr int kOffBar = kOffP + 4 * kPer * kRowBlock;
-  // kv_full[S], kv_empty[S], q_full, s_full[2], p_full[2], rows_full[R], rows_empty[R]
+  // kv_full[S], kv_empty[S], q_full, s_full[2], p_full[2], rows_full[R], rows_empty[R], scaled[R]
   static constexpr int kRing = 8;  // tiles that the page lookup may be ahead
-  static constexpr int kNumBars = 2 * kSlots + 5 + 2 * kRing;
+  static constexpr int kNumBars = 2 * kSlots + 5 + 3 * kRing;
   static constexpr int kOffMisc = kOffBar + ((kNumBars * 8 + 15) & ~15);
   static constexpr int kOffRows = kOffMisc + 64;
   // per row: factor, limit, threshold, reference, rescale, running max, output row; per warp and row: two sums
@@ -136,34 +137,48 @@ __device__ __forceinline__ int row_tiles(const PagedArgs& a, int nq) {
 // Tiles of one unit of a sequence (one, fully masked, when it has no key).
 __device__ __forceinline__ int unit_tiles(int lk) { return max(1, (lk + kTile - 1) / kTile); }
 
-// This CTA's (its team's) stretch [pos, end) of the line of tiles, as pieces of units.
+// A unit's start and end (Q in, O out, the pipeline filled and drained) take about as long as
+// some tiles; each unit counts as many more, at its beginning, so that a CTA with the end of
+// one unit and the beginning of the next is not 2.5 us behind the others.  One sequence of
+// 8192 keys, 32 heads, with 0, 2, 3, 4 and 6 in 8 bits: 24.5, 23.4, 23.2, 22.6 and 23.4 us;
+// 16 sequences of 8 key heads of 64: 49.9, 40.1, 40.1, 38.9 and 39.4 us; with 0, 1, 2 and 3 in
+// bf16 32.0, 31.1, 31.0 and 31.2 us.
+template <bool kQ8>
+constexpr int kUnitCost = kQ8 ? 4 : 2;
+
+// This CTA's (its team's) stretch [pos, end) of the line of what units count, as pieces of
+// units.
 struct Work {
   long long pos, end, total;
-  int b, off;  // sequence of pos, and pos's place among its tiles
+  int b, off;  // sequence of pos, and pos's place in what its units count
   int teams;   // teams that have a stretch
 };
 struct Piece {
   int b, hg, rt, t0, t1, tiles;
+  int after;  // of what the unit counts, behind the stretch
   SeqInfo s;
 };
-template <int N, int D>
+template <int N, bool kQ8, int D>
 __device__ __forceinline__ bool next_piece(const PagedArgs& a, Work& w, Piece& p) {
   if (w.pos >= w.end) return false;
   for (; w.b < a.B; ++w.b) {
     p.s = seq_info(a, w.b);
     const int rts = row_tiles<N, D>(a, p.s.nq);
     p.tiles = unit_tiles(p.s.lk);
-    const int cost = rts * a.sets * p.tiles;
+    const int each = p.tiles + kUnitCost<kQ8>, cost = rts * a.sets * each;
     if (w.off < cost) {
-      const int u = w.off / p.tiles;
+      const int u = w.off / each, at = w.off - u * each;
+      const int n = (int)min((long long)(each - at), w.end - w.pos);
+      p.t0 = max(0, at - kUnitCost<kQ8>);
+      p.t1 = at + n - kUnitCost<kQ8>;
+      p.after = each - at - n;
+      w.pos += n;
+      w.off += n;
+      if (p.t1 <= p.t0) return false;  // only of what the unit counts more: the next CTA begins it
       p.b = w.b;
       const int set = u / rts;
       p.hg = set * a.team + (int)blockIdx.x % a.team;
       p.rt = u - set * rts;
-      p.t0 = w.off - u * p.tiles;
-      p.t1 = (int)min((long long)p.tiles, p.t0 + (w.end - w.pos));
-      w.pos += p.t1 - p.t0;
-      w.off += p.t1 - p.t0;
       return true;
     }
     w.off -= cost;
@@ -172,14 +187,14 @@ __device__ __forceinline__ bool next_piece(const PagedArgs& a, Work& w, Piece& p
 }
 
 // Run by one warp: the line's length and where this CTA's stretch begins.
-template <int N, int D>
+template <int N, bool kQ8, int D>
 __device__ __forceinline__ Work find_work(const PagedArgs& a) {
   const int lane = lane_id();
   Work w;
   auto cost_of = [&](int b) {
     if (b >= a.B) return 0;
     const SeqInfo s = seq_info(a, b);
-    return row_tiles<N, D>(a, s.nq) * a.sets * unit_tiles(s.lk);
+    return row_tiles<N, D>(a, s.nq) * a.sets * (unit_tiles(s.lk) + kUnitCost<kQ8>);
   };
   long long total = 0;
   for (int b = lane; b < a.B; b += 32) {
@@ -283,6 +298,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
   uint64_t* p_full = q_full + 3;
   uint64_t* rows_full = q_full + 5;
   uint64_t* rows_empty = rows_full + L::kRing;
+  uint64_t* scaled = rows_empty + L::kRing;
   uint32_t* ring_rows = reinterpret_cast<uint32_t*>(smem + L::kOffRing);
   volatile int* ring_tile = reinterpret_cast<volatile int*>(smem + L::kOffTile);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
@@ -304,7 +320,8 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
       mbar_init(p_full + i, 4);
     }
     for (int i = 0; i < L::kRing; ++i) {
-      mbar_init(rows_full + i, kQ8 ? 33 : 1);  // the lookup warp, in 8 bits also its lanes' scale copies
+      mbar_init(rows_full + i, 1);
+      mbar_init(scaled + i, 32);  // the lookup warp's lanes, 8 bits only
       mbar_init(rows_empty + i, kLoaders<N> + (kQ8 ? 4 : 0));  // the loaders, and the softmax warps for the scales' words
     }
     *abort_flag = 0;
@@ -319,7 +336,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
   // up to here the kernel before may still run
   grid_dependency_wait();
   if (warp == 2) {
-    const Work w = find_work<N, D>(a);
+    const Work w = find_work<N, kQ8, D>(a);
     if (lane == 0) {
       *work = w;
       a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -337,10 +354,10 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
 
   if (warp == 1) {
     // -------------------------------------------------------------------- page lookup
-    const PageRing ring{ring_rows, ring_tile, smem_u32(smem + L::kOffScales), rows_full, rows_empty};
+    const PageRing ring{ring_rows, ring_tile, smem_u32(smem + L::kOffScales), rows_full, scaled, rows_empty};
     const bool ok = look_up_pages<L::kRing, kQ8, D == 64>(a, ring, abort_flag, [&](int& b, int& hg, int& t0, int& t1, int& lk) {
       Piece p;
-      if (!next_piece<N, D>(a, w, p)) return false;
+      if (!next_piece<N, kQ8, D>(a, w, p)) return false;
       b = p.b, hg = p.hg, t0 = p.t0, t1 = p.t1, lk = p.s.lk;
       return true;
     });
@@ -459,7 +476,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
         }
       };
       Piece p;
-      while (ok && next_piece<N, D>(a, w, p)) {
+      while (ok && next_piece<N, kQ8, D>(a, w, p)) {
         if (!wait(q_full, piece++ & 1)) break;
         tc_fence_after();
         const int tiles = p.t1 - p.t0;
@@ -534,7 +551,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
       }
     };
     Piece p;
-    while (next_piece<N, D>(a, w, p)) {
+    while (next_piece<N, kQ8, D>(a, w, p)) {
       const int tiles = p.t1 - p.t0;
       // ---- the piece's rows: kThreadsPerRow threads share a row of 128 dims
       {
@@ -635,6 +652,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
           if (u >= n_tiles) break;
           if constexpr (kQ8) {
             const uint32_t at = (c + u) % L::kRing, rw = ring_rows[at * kTile + r];
+            wait(scaled + at, ((c + u) / L::kRing) & 1);
             uint4 words;
             if constexpr (D == 64) {
               words = reinterpret_cast<const uint4*>(smem + L::kOffScales)[at * kTile + r];
@@ -824,8 +842,8 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
         }
         if (p.t0 == 0 && tid < N) a.part_rows[(size_t)blockIdx.x * N + tid] = out_row[tid];
         if (p.t0 == 0 && tid == 0) {
-          // parts up to the team that has the unit's last tile
-          const long long last = w.pos - p.t1 + p.tiles - 1;
+          // parts up to the team that has the unit's end
+          const long long last = w.pos + p.after - 1;
           a.meta[blockIdx.x] =
               make_int4((int)(((last + 1) * w.teams - 1) / w.total) - (int)blockIdx.x / a.team + 1, 0, 0, 0);
         }
@@ -861,11 +879,26 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
   float M = -INFINITY, acc[kPer], l = 0.f, lr = 0.f;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  for (int i0 = 0; i0 < parts; i0 += 32) {
+  constexpr int kBatch = 16;
+  for (int i0 = 0; i0 < parts; i0 += kBatch) {
     // lane i: the sums of part i0 + i
-    const bool have = i0 + lane < parts;
+    const bool have = lane < kBatch && i0 + lane < parts;
     const size_t own = at(have ? i0 + lane : 0);
     const float pl = have ? a.part_l[own] : 0.f, pm = have ? a.part_m[own] : -INFINITY, plr = have ? a.part_lr[own] : 0.f;
+    // and everyone its dims of all of them
+    float x[kBatch][kPer];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (i0 + i >= parts) break;
+      const float* src = a.part_o + at(i0 + i) * 128 + d0;
+      if constexpr (kPer == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        x[i][0] = v.x, x[i][1] = v.y;
+      }
+    }
     const float top = fmaxf(M, redux_max(pl == 0.f ? -INFINITY : pm));
     const float keep = M == -INFINITY ? 0.f : ex2(M - top);
     const float wt = pl == 0.f ? 0.f : ex2(pm - top);
@@ -874,20 +907,12 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
     lr = lr * keep + wt * plr;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] *= keep;
-#pragma unroll 8
-    for (int i = 0; i < min(32, parts - i0); ++i) {
-      const float w = __shfl_sync(0xffffffffu, wt, i);
-      const float* src = a.part_o + at(i0 + i) * 128 + d0;
-      float x[kPer];
-      if constexpr (kPer == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        x[0] = v.x, x[1] = v.y;
-      }
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+    for (int i = 0; i < kBatch; ++i) {
+      if (i0 + i >= parts) break;
+      const float w = __shfl_sync(0xffffffffu, wt, i);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, x[i][e], acc[e]);
     }
   }
 #pragma unroll
