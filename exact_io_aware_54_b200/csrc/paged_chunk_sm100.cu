@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       });
       ok = ok && fine;
       if (!ok && lane == 0) give_up();
-    } else if (warp == 0 && lane == 0) {
+    } else if (warp == 0 && elect_one()) {
       // ------------------------------------------------------------------ MMA issuer
       const uint32_t base = smem_u32(smem);
       const SDesc q_desc[2] = {sdesc_make(base, 16, 1024), sdesc_make(base + L::kTileBytes, 16, 1024)};
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           if (t == 0 || rows > 128) umma_commit(o_done + t);
         mbar_arrive(piece_empty + n % L::kPieces);
       }
-    } else if (kQ8 && warp >= 8 - kLoaders<D, kQ8>) {
+    } else if (kQ8 && warp != 0 && warp >= 8 - kLoaders<D, kQ8>) {
       load_tiles();
     }
   } else if (!kQ8 && warp < 8) {

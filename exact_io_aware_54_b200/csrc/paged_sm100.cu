@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
     if (!ok && lane == 0) give_up();
   } else if (warp == 0) {
     // -------------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kIdescS = kQ8 ? idesc_e4m3_f32(128, 2 * N, false, false) : idesc_bf16_f32(128, N, false, false);
       constexpr uint32_t kIdescO = kQ8 ? idesc_e4m3_f32(128, 2 * N, true, true) : idesc_bf16_f32(128, N, true, true);
       const uint32_t base = smem_u32(smem);
