@@ -486,6 +486,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         if (lane == 0) *piece_at(n) = p;
         mbar_arrive_warp(piece_full + n % L::kPieces);
         ++n;
+        // its rows of Q into L2, some tiles before they are wanted
+        const int rows = p.tiles == 0 ? 0 : min(kUnitRows, p.s.nq * a.G - p.unit * kUnitRows);
+#pragma unroll 1
+        for (int i = lane; i < rows; i += 32) {
+          const int row = p.unit * kUnitRows + i, token = token_of_row(a, row);
+          const __nv_bfloat16* from = a.q + (long long)(p.s.qoff + token) * a.q_stride + (long long)(p.hk * a.G + row - token * a.G) * D;
+          prefetch_l2(from);
+          if (D == 128) prefetch_l2(from + 64);
+        }
       };
       bool ok = look_up_pages<L::kRing, kQ8, false>(a, ring, abort_flag, [&](int& b, int& hk, int& t0, int& t1, int& lk) {
         Piece p;
@@ -527,22 +536,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         const int rows = p.s.nq * a.G - p.unit * kUnitRows;
         const int nt[2] = {min(t1, tiles_of(keys_of(a, p.s, p.unit * kUnitRows + 127))), rows > 128 ? t1 : t0};
         bool have[2] = {t0 < nt[0], t0 < nt[1]};
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (t == 0 || rows > 128) {
-            if (!wait(q_full + t, q_cnt[t]++ & 1)) break;
-          }
-        if (!ok) break;
-        tc_fence_after();
         if (!slot_ready(g)) break;
         {
           const SDesc k = SDesc{ring_k.lo + (g % L::kStages) * kSlot16, ring_k.hi};
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2; ++t) {
+            if (t == 0 || rows > 128) {
+              if (!wait(q_full + t, q_cnt[t]++ & 1)) break;
+              tc_fence_after();
+              if (!have[t]) umma_commit(o_done + t);  // nothing to do for it
+            }
             if (have[t]) {
               issue_qk<D>(tmem + tm_s(t), q_desc[t], k);
               umma_commit(s_full + t);
             }
+          }
+          if (!ok) break;
           umma_commit(kv_empty + g % L::kStages);
           ++g;
         }
@@ -565,6 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
               tc_fence_after();
               ++p_cnt[t];
               issue_pv_half<D>(tmem + tm_o<D>(t), tmem + tm_s(t), v, true, 1);
+              // a row tile's end and its next beginning overlap the other's last tile
+              if (j + 1 == nt[t]) umma_commit(o_done + t);
             }
             if (more && j + 1 < nt[t]) {
               issue_qk<D>(tmem + tm_s(t), q_desc[t], k);
@@ -579,9 +590,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           }
         }
         if (!ok) break;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (t == 0 || rows > 128) umma_commit(o_done + t);
         mbar_arrive(piece_empty + n % L::kPieces);
       }
     } else if (kQ8 && warp != 0 && warp >= 8 - kLoaders<D, kQ8>) {
@@ -622,21 +630,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       {
         const long long from = mine ? (long long)(p.s.qoff + token) * a.q_stride + (long long)head * D : -1;
         const int chunk = lane % kLanes, sub = lane / kLanes;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {  // 16 rows at a time
-          uint4 x[16 / kRowsAtOnce];
-#pragma unroll
-          for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
-            const long long src = __shfl_sync(0xffffffffu, from, h * 16 + i * kRowsAtOnce + sub);
-            x[i] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.q + src) + chunk) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
-            const int rr = quarter * 32 + h * 16 + i * kRowsAtOnce + sub;
-            st_shared_v4(q_tile + (chunk >> 3) * L::kBoxBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4), x[i].x, x[i].y,
-                         x[i].z, x[i].w);
-          }
+#pragma unroll 4
+        for (int i = 0; i < 32; i += kRowsAtOnce) {
+          const long long src = __shfl_sync(0xffffffffu, from, i + sub);
+          const int rr = quarter * 32 + i + sub;
+          cp_async16_or_zero(q_tile + (chunk >> 3) * L::kBoxBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4),
+                             a.q + (src >= 0 ? src : 0) + chunk * 8, src >= 0);
         }
+        cp_async_wait_all();
       }
       fence_proxy_async_smem();
       mbar_arrive_warp(q_full + t);
