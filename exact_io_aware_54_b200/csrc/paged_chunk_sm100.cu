@@ -10,8 +10,8 @@
 //
 //  * Rows.  The softmax threads load their own row of Q (any token stride, any G) into the
 //    swizzled tile and store their own row of O; a row's limit follows from its token.
-//  * Keys.  Pages are looked up by the warp of paged_common.cuh; four loader warps fill
-//    the K and V tiles, each 32 keys of every tile.  bf16: 16-byte asynchronous copies.
+//  * Keys.  Pages are looked up by the warp of paged_common.cuh; loader warps fill
+//    the K and V tiles, each its keys of every tile.  bf16: 16-byte asynchronous copies.
 //    8 bit: each lane loads 16 codes, multiplies by the row's scale and stores 16 bf16
 //    values, all of the tile times 2^-60, which the softmax scale and the final 1 / l make
 //    up for.  A code times its power of two is a bf16 number, so the softmax warps, which
@@ -21,13 +21,14 @@
 //    parts, one per CTA (one CTA per SM).  A unit cut by a border leaves fp32 partial
 //    states of its 256 rows, two at most per CTA, which a second kernel joins in order.
 //    512 tokens over 16K keys (8 key heads, G = 4) are 64 units for 148 CTAs.
-//  * What it measures: 8192 causal tokens over themselves (32 heads of 128, bf16) 663 us,
-//    where the packed forward without pages (fa_fwd_varlen) takes 578: the exponentials and
-//    the chain from scores to weights bound both, and the rest is the pieces' starts and
-//    ends.  512 tokens over 16K keys (8 key heads): bf16 167 us, 8 bit 224, where the
-//    conversion of the tiles by the loader warps bounds it.
-//  * Warp roles (512 threads): 0 MMA issuer, 1 page lookup, 4-7 loaders, 8-11 and 12-15
-//    the softmax groups of the two row tiles.
+//  * What it measures: 8192 causal tokens over themselves (32 heads of 128, bf16) 620 us, 886
+//    TFLOP/s: the chain from scores to weights to the next scores bounds it, as it does the
+//    dense forward (3600 of a tile's 4360 cycles; the products take 2100).  16 ragged
+//    sequences of 64-wide heads 141 us.  512 tokens over 16K keys (8 key heads), 8 bit:
+//    198 us, where the conversion of the tiles by the loader warps bounds it (5900 cycles a
+//    tile).
+//  * Warp roles (512 threads): 0 MMA issuer, 1 page lookup, 4-7 loaders (8 bits, d = 128:
+//    2-7), 8-11 and 12-15 the softmax groups of the two row tiles.
 #include "paged_common.cuh"
 
 namespace fa {
@@ -104,7 +105,10 @@ __device__ __forceinline__ int units_of(const PagedArgs& a, int nq) {
 }
 // A unit's start and end (Q in, O out, the pipeline filled and drained) take about as long as
 // two or three tiles, so each unit counts kUnitCost tiles more, at its beginning: without
-// them the CTAs of many short units (a prompt's first rows) came 13% after the mean.
+// them the CTAs of many short units (a prompt's first rows) came 13% after the mean.  (1, 2, 3
+// and 4: 165, 146, 147 and 144 us for 16 ragged sequences of 64-wide heads, 617 to 652 us for
+// 8192 tokens without an order.  Counting a tile of a unit with up to 128 rows four fifths of
+// another won 2% of the ragged sequences.)
 constexpr int kUnitCost = 3;
 // Tiles of unit u of a key head, and what it counts.
 __device__ __forceinline__ int unit_tiles(const PagedArgs& a, const SeqInfo& s, int u) {

@@ -44,11 +44,12 @@
 //    may round to nothing in the product and still count fully in the sum.
 //  * Work split: CTAs come in teams of neighbouring key heads, which read the same keys'
 //    neighbouring bytes at about the same time: a head's slice of a row is only 128 bytes in
-//    8 bits (64 requests of 8 key heads: 262 us without teams, 253 in teams of 2, 4 or 8).  A (sequence, team's heads, row tile) unit counts ceil(L / 128) tiles and
-//    kUnitCost for its start and end; the line of all units is cut into equal parts, one per team (one CTA per SM), whatever
-//    the lengths.  A unit that lies in one part is finished there; others leave fp32
-//    partial states, two at most per CTA, that paged_merge_kernel joins in order.  No
-//    atomics: results do not depend on timing.
+//    8 bits (64 requests of 8 key heads: 262 us without teams, 253 in teams of 2, 4 or 8).
+//    A (sequence, team's heads, row tile) unit counts ceil(L / 128) tiles and kUnitCost for
+//    its start and end; the line of all units is cut into equal parts, one per team (one CTA
+//    per SM), whatever the lengths.  A unit that lies in one part is finished there; others
+//    leave fp32 partial states, two at most per CTA, that paged_merge_kernel joins in order.
+//    No atomics: results do not depend on timing.
 //  * Warp roles: 0 MMA issuer, 1 page lookup, then K loaders, V loaders, and four warps for
 //    softmax and epilogue.  The lookup warp turns tiles into rows of the cache, up to eight tiles
 //    ahead, in a ring that the loaders copy from, and fetches the rows' scale bytes: as the
@@ -57,11 +58,11 @@
 //  * Every role is a small loop: one warp of each runs per scheduler, and with the loaders'
 //    loops unrolled (2000 instructions each) two fifths of all stalls were for instructions
 //    not yet fetched (64 requests, 8 key heads: 499 us; 272 with small loops over a ring of rows).
-//  * What it measures: 64 requests of 512 to 16384 keys, 32 query and 8 key heads of 128, 8 bit: 223 us, 85% of
-//    the measured copy rate; bound by the softmax and MMA chain of a tile, which then takes
-//    about as long as its bytes.  One sequence of 8192 keys, 32 heads: 22.6 us for 10 us of
-//    bytes, the rest the start (four dependent loads: offsets, page, keys, then the first scores:
-//    5.5 us), the epilogue and the join (1 and 3 us).
+//  * What it measures: 64 requests of 512 to 16384 keys, 32 query and 8 key heads of 128, 8
+//    bit: 224 us, 85% of the measured copy rate; bound by the softmax and MMA chain of a tile,
+//    which takes about as long as its bytes.  One sequence of 8192 keys, 32 heads: 22.5 us for
+//    10 us of bytes, the rest the start (four dependent loads, lengths, page, keys, and the
+//    first scores: 5.5 us), the epilogue and the join (1 and 3 us).
 //  * Few waits: the issue order Q K^T of step s + 1, then P V of step s, makes the scores'
 //    barrier of a step imply that the products of two steps before have read their
 //    weights, and the weights' barrier that the scores have been read; the barrier that
