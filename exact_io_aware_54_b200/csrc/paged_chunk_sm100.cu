@@ -25,7 +25,7 @@
 //    TFLOP/s: the chain from scores to weights to the next scores bounds it, as it does the
 //    dense forward (3600 of a tile's 4360 cycles; the products take 2100).  16 ragged
 //    sequences of 64-wide heads 141 us.  512 tokens over 16K keys (8 key heads), 8 bit:
-//    198 us, where the conversion of the tiles by the loader warps bounds it (5900 cycles a
+//    203 us, where the conversion of the tiles by the loader warps bounds it (6000 cycles a
 //    tile).
 //  * Warp roles (512 threads): 0 MMA issuer, 1 page lookup, 4-7 loaders (8 bits, d = 128:
 //    2-7), 8-11 and 12-15 the softmax groups of the two row tiles.
@@ -283,14 +283,20 @@ __device__ __forceinline__ void issue_pv_half(uint32_t o_tmem, uint32_t p_tmem, 
 // multiplication is left: by 2^(e + 120), of which bf16 holds 2^(e + 60) for every e in
 // [-60, 60].  (The smallest product, 2^-9 of the lowest scale, is 2^-129: a bf16 subnormal,
 // still exact.)
-__device__ __forceinline__ uint32_t dequantise2(uint32_t t, uint32_t f) {
-  const uint32_t x = (t & 0x80008000u) | ((t >> 4) & 0x07F007F0u);
+// m: the magnitudes moved down; 0x7F0 tells of a NaN (code 127), which comes out as a number.
+__device__ __forceinline__ uint32_t dequantise2(uint32_t t, uint32_t f, uint32_t& m) {
+  m = (t >> 4) & 0x07F007F0u;
+  const uint32_t x = (t & 0x80008000u) | m;
   uint32_t y;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f));
   return y;
 }
-__device__ __forceinline__ uint2 dequantise4(uint32_t q, uint32_t f) {
-  return make_uint2(dequantise2(__byte_perm(q, 0, 0x1404), f), dequantise2(__byte_perm(q, 0, 0x3424), f));
+// Four codes; top: the largest m so far in either half.
+__device__ __forceinline__ uint2 dequantise4(uint32_t q, uint32_t f, uint32_t& top) {
+  uint32_t m0, m1;
+  const uint2 y = make_uint2(dequantise2(__byte_perm(q, 0, 0x1404), f, m0), dequantise2(__byte_perm(q, 0, 0x3424), f, m1));
+  top = __vimax3_u16x2(top, m0, m1);
+  return y;
 }
 
 template <int D, bool kQ8>
@@ -428,11 +434,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             const uint32_t cut = ((row[j] * (uint32_t)a.Hkv + hk) & 3u) * 8;
             // past the sequence's end the codes are zeros, and the word holds anything
             const uint32_t f = row[j] != kNoRow ? ((((word[j] >> cut) & 0xFFu) + 60u) << 7) * 0x00010001u : 0u;
-            const uint2 w0 = dequantise4(x[j].x, f), w1 = dequantise4(x[j].y, f), w2 = dequantise4(x[j].z, f),
-                        w3 = dequantise4(x[j].w, f);
+            uint32_t top = 0;
+            const uint2 w0 = dequantise4(x[j].x, f, top), w1 = dequantise4(x[j].y, f, top),
+                        w2 = dequantise4(x[j].z, f, top), w3 = dequantise4(x[j].w, f, top);
             const uint32_t to = tile + key * 128, c2 = 2 * (chunk & 3);  // 16-byte chunks of the bf16 row: c2 and c2 + 1
             st_shared_v4(to + ((c2 ^ (key & 7)) << 4), w0.x, w0.y, w1.x, w1.y);
             st_shared_v4(to + (((c2 + 1) ^ (key & 7)) << 4), w2.x, w2.y, w3.x, w3.y);
+            if (((top + 0x00100010u) & 0x08000800u) != 0) {  // NaN among the 16: once more, one by one
+#pragma unroll 1
+              for (int i = 0; i < 16; ++i)
+                if ((ld_shared_u8(codes + (i0 + j) * 512 + i) & 0x7F) == 0x7F)
+                  st_shared_u16(to + (((c2 + i / 8) ^ (key & 7)) << 4) + (i % 8) * 2, 0x7FC0);
+            }
           }
 #pragma unroll
           for (int j = 0; j < kTogether; ++j) {

@@ -216,6 +216,39 @@ def test_chunk_scale_ends(n, power):
     _chunk(c, 4, [n], 127)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("n", [1, 150])
+def test_chunk_not_finite(n, q8, d):
+    """A NaN in the cache comes out as one: of a key, in every token that sees it; of a value, in its dims."""
+    L, at, head = 300, 20, 1
+    c = Cache(150, [L], 2, d, 16, q8)
+    page, row = int(c.table[0, at // 16]), at % 16
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    q = synth._normal((n, 4, d), 151).cuda()
+    call = lambda: fa.fa_fwd_paged(q, c.pages["k"], c.pages["v"], cu, c.table, c.seqlens, n, L, True, **c.kw)
+    good, _ = call()
+    mine = torch.arange(4, device="cuda") // 2 == head
+    for name, dims in (("v", [0, 5, 17, d - 1]), ("k", [d // 2 + 3])):
+        pages = c.pages[name].view(torch.uint8) if q8 else c.pages[name]
+        old = pages.clone()
+        for i in dims:
+            pages[page, row, head, i] = (0x7F if i % 2 else 0xFF) if q8 else math.nan
+        o, lse = call()
+        _check()
+        pages.copy_(old)
+        if name == "k":
+            assert o[:, mine].isnan().all() and lse[mine].isnan().all()
+            if d == 128:
+                assert torch.equal(o[:, ~mine], good[:, ~mine])
+        else:
+            hit = torch.zeros(d, dtype=torch.bool, device="cuda")
+            hit[dims] = True
+            assert o[:, mine][..., hit].isnan().all()
+            assert torch.equal(o[:, mine][..., ~hit], good[:, mine][..., ~hit])
+            assert torch.equal(o[:, ~mine], good[:, ~mine])
+
+
 def test_workspace_is_the_streams():
     """A bad page is recorded where fa_check looks on that stream, and nowhere else."""
     c = Cache(128, [40], 1, 64, 16, True)
