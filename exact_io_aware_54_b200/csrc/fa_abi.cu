@@ -682,7 +682,7 @@ static bool paged_sizes_ok(int B, int Hq, int Hkv, int max_seqlen_q, int max_seq
   // rows of a chunk, and one sequence's 128-key tiles times its row tiles, in 32 bits
   const long long rows = (long long)max_seqlen_q * (Hq / Hkv);
   return rows < (1LL << 31) &&
-         (rows / 32 + 1) * Hkv < (1LL << 31) / ((long long)max_seqlen_k / 128 + 1) && Hq < (1 << 16);
+         (rows / 32 + 1) * Hkv < (1LL << 31) / ((long long)max_seqlen_k / 128 + 8) && Hq < (1 << 16);
 }
 
 // Rows per key head up to which a sequence goes to the few-row kernel: one tile of its 32

@@ -553,6 +553,49 @@ def test_streams_and_graphs(n):
     del graphs
 
 
+@pytest.mark.parametrize("n", [1, 150])
+def test_graph_behind_other_work(n):
+    """Captured behind a memset, another stream's work joined right before the call, and a write of
+    the cache: the kernels' early start waits for all of it."""
+    c, L = Cache(270, [700], 2, 128, 16, True), 700
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    a, b = (synth._normal((n, 8, 128), 271 + i).cuda() for i in range(2))
+    new = synth._normal((n, 2, 128), 273).cuda()
+    q, x = torch.empty_like(a), torch.empty_like(a)
+    args = (c.pages["k"], c.pages["v"], cu, c.table, c.seqlens, n, L, True)
+    write = lambda: fa.fa_cache_write(x[:, :2], x[:, 2:4], c.pages["k"], c.pages["v"], cu, c.table, c.seqlens, **c.kw)
+
+    def step(side):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        x.zero_()
+        with torch.cuda.stream(side):
+            q.copy_(a)
+            for _ in range(20):
+                q.add_(b)
+        x[:, :4].add_(new.repeat(1, 2, 1))
+        write()
+        main.wait_stream(side)
+        out = fa.fa_fwd_paged(q, *args, **c.kw)
+        q.zero_()  # behind the call, which has read it
+        return out
+
+    side = torch.cuda.Stream()
+    want = step(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(side)
+    for _ in range(5):
+        got[0].fill_(9)
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    _check()
+    del g
+
+
 def test_launch_names():
     """The calls run the library's own kernels."""
     import ctypes
