@@ -685,17 +685,17 @@ static bool paged_sizes_ok(int B, int Hq, int Hkv, int max_seqlen_q, int max_seq
          (rows / 32 + 1) * Hkv < (1LL << 31) / ((long long)max_seqlen_k / 128 + 8) && Hq < (1 << 16);
 }
 
-// Rows per key head up to which a sequence goes to the few-row kernel: one tile of its 32
-// (d = 64: two heads share it).  16 sequences of 4000 keys, 32 key heads, 32 tokens: 219 us
-// (bf16) and 297 (8 bit) there, 320 and 406 in the chunk kernel; with 64 tokens 386 and 528
-// against 322 and 408.
-static int paged_few_rows(int d) { return d == 64 ? 16 : 32; }
+// Rows per key head up to which a sequence goes to the few-row kernel: one tile of its 32 (d =
+// 64, where two heads share a tile: two).  16 sequences of 4000 keys, no groups, there and in
+// the chunk kernel: 32 heads of 128, 32 tokens 176 and 245 us (bf16), 259 and 354 (8 bit), 40
+// tokens 331 and 244, 490 and 355; 16 heads of 64, 32 tokens 95 and 113, 138 and 140.
+constexpr int kPagedFewRows = 32;
 
 size_t fa_paged_workspace_size(int B, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int d) {
   if (!paged_sizes_ok(B, Hq, Hkv, max_seqlen_q, max_seqlen_k) || (d != 64 && d != 128)) return 0;
   // both kernels' states in the same place: they run one after the other
   const size_t few = paged_few_workspace();
-  if ((long long)max_seqlen_q * (Hq / Hkv) <= paged_few_rows(d)) return few;
+  if ((long long)max_seqlen_q * (Hq / Hkv) <= kPagedFewRows) return few;
   return std::max(few, paged_chunk_workspace(d));
 }
 
@@ -749,7 +749,7 @@ static fa_status fwd_paged(const void* q, long long q_row_stride, const void* k_
   a.scale = resolve_scale(softmax_scale, d);
   a.workspace = workspace;
   a.timeout_ns = wait_timeout_ns();
-  a.few_rows = paged_few_rows(d);
+  a.few_rows = kPagedFewRows;
   // A batch of short and long chunks: each kernel takes its own sequences (the lengths are
   // on the device) and passes over the others.
   const bool some_many = (long long)max_seqlen_q * (Hq / Hkv) > a.few_rows;
