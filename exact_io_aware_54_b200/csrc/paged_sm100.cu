@@ -76,11 +76,13 @@ using namespace paged;
 namespace {
 
 // Loader warps, half of them for K.  One warp each takes about 1050 cycles for a tile of 8
-// bit keys, as long as its bytes do: two are never ahead.  With 32 rows the softmax takes longer and needs the registers.
-template <int N>
-constexpr int kLoaders = N == 16 ? 4 : 2;
-template <int N>
-constexpr int kThreads = (2 + kLoaders<N> + 4) * 32;
+// bit keys, as long as its bytes do: two are never ahead (eight: 234 us for 64 requests, four
+// 228).  With 32 rows the 8 bit softmax takes longer and needs the registers: 32 tokens, 16 x
+// 4000 keys, 32 heads of 128, with two and four 259 and 289 us, in bf16 177 and 174.
+template <int N, bool kQ8>
+constexpr int kLoaders = kQ8 && N == 32 ? 2 : 4;
+template <int N, bool kQ8>
+constexpr int kThreads = (2 + kLoaders<N, kQ8> + 4) * 32;
 // Exponent offset and threshold of the running maximum, log2 units.  8 bit: weights
 // up to 2^(7 + 1) use e4m3's range (448) and leave the second piece a floor of
 // 2^-10 / 2^7.  bf16: as in the dense forward.
@@ -280,7 +282,7 @@ __device__ __forceinline__ float warp_sums(float (&v)[N]) {
 // to a key head, or one, and a single token: most decoding.  With the other rows' scores
 // left in place the softmax loop is a quarter of its instructions.)
 template <int N, bool kQ8, int D, int kLive>
-__global__ void __launch_bounds__(kThreads<N>, 1)
+__global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
     paged_kernel(const PagedArgs a) {
   using L = PagedLayout<N, kQ8>;
   using R = SoftmaxRange<kQ8>;
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(kv_full + s, kLoaders<N> / 2);  // the warps that share a tile
+      mbar_init(kv_full + s, kLoaders<N, kQ8> / 2);  // the warps that share a tile
       mbar_init(kv_empty + s, 1);
     }
     mbar_init(q_full, 4);
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
     for (int i = 0; i < L::kRing; ++i) {
       mbar_init(rows_full + i, 1);
       mbar_init(scaled + i, 32);  // the lookup warp's lanes, 8 bits only
-      mbar_init(rows_empty + i, kLoaders<N> + (kQ8 ? 4 : 0));  // the loaders, and the softmax warps for the scales' words
+      mbar_init(rows_empty + i, kLoaders<N, kQ8> + (kQ8 ? 4 : 0));  // the loaders, and the softmax warps for the scales' words
     }
     *abort_flag = 0;
     *group_dead = 0;
@@ -363,9 +365,9 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
       return true;
     });
     if (!ok && lane == 0) give_up();
-  } else if (warp >= 2 && warp < 2 + kLoaders<N>) {
+  } else if (warp >= 2 && warp < 2 + kLoaders<N, kQ8>) {
     // -------------------------------------------------------------------- K and V loaders
-    constexpr int kParts = kLoaders<N> / 2;  // warps that share a tile
+    constexpr int kParts = kLoaders<N, kQ8> / 2;  // warps that share a tile
     const bool is_v = warp >= 2 + kParts;
     const int part = (warp - 2) % kParts;
     const uint32_t row_bytes = (uint32_t)a.Hkv * D * (kQ8 ? 1 : 2);
@@ -512,7 +514,7 @@ __global__ void __launch_bounds__(kThreads<N>, 1)
     // -------------------------------------------------------------------- softmax and epilogue
     const uint32_t quarter = warp & 3;
     const int r = quarter * 32 + lane;         // key of the tile, then dim of O
-    const int tid = threadIdx.x - 64 - 32 * kLoaders<N>;  // 0 .. 127
+    const int tid = threadIdx.x - 64 - 32 * kLoaders<N, kQ8>;  // 0 .. 127
     const uint32_t lanes = (quarter * 32) << 16;
     float* factor = reinterpret_cast<float*>(smem + L::kOffRows);  // of the scores: scale, log2 e, Q's scale
     int* limit = reinterpret_cast<int*>(factor + N);               // first key that the row does not see
@@ -963,7 +965,7 @@ fa_status launch_paged_impl(const PagedLaunch& L0, cudaStream_t stream) {
   c.place(a, L0.workspace);
   prof_before(stream, kKPaged);
   cudaError_t err =
-      launch_dependent(paged_kernel<N, kQ8, D, kLive>, dim3(a.teams * a.team), kThreads<N>, L::kSmemBytes, stream, a);
+      launch_dependent(paged_kernel<N, kQ8, D, kLive>, dim3(a.teams * a.team), kThreads<N, kQ8>, L::kSmemBytes, stream, a);
   prof_after(stream, kKPaged);
   if (err != cudaSuccess) return FA_ERR_CUDA;
   if (L0.max_k <= kTile) return FA_OK;  // units of one tile are never split
