@@ -20,10 +20,13 @@
 //    multiplied by kind::f8f6f4 MMAs.  The bf16 row of Q is split into two e4m3
 //    pieces, q = q1 + q2: four significant bits each make bf16's eight, exact but
 //    for elements under 2^-9 of the row's largest, off by at most 2^-17 of it (e4m3's
-//    subnormal step).  The weights are split the same way, p = p1 + p2, off by at most
-//    2^-8 of p, as in bf16, or 2^-17 of the row's largest weight.  The two pieces of a row
-//    are two columns of the product, added up when they are read: an MMA costs the same
-//    for 32 or 64 columns as for 16, so a second pass over the tile would cost twice.
+//    subnormal step).  A weight is an fp16 number cut into three e5m2 pieces (three
+//    significant bits each, e5m2 being the upper byte of fp16), p = p1 + p2 / 8 + p3 / 64,
+//    off by at most 2^-9 + 2^-11 of p, or 2^-36 of the row's largest weight: many weak keys
+//    beside a strong one count as they do in bf16 weights.  (Two e4m3 pieces lose weights
+//    under 2^-17 of the largest, of which a long cache has enough to matter.)  The pieces of
+//    a row are columns of the product, added up when they are read: an MMA costs the same
+//    for 32 or 64 columns as for 16, so another pass over the tile would cost as much again.
 //    The key scales multiply the scores in fp32; the value scales 2^e_j are carried
 //    in the weights: with y_j = x_j log2(e) + e_j the weight is 2^(y_j - m), m the
 //    running maximum of y, and the sum takes it times 2^-e_j.
@@ -84,11 +87,11 @@ constexpr int kLoaders = kQ8 && N == 32 ? 2 : 4;
 template <int N, bool kQ8>
 constexpr int kThreads = (2 + kLoaders<N, kQ8> + 4) * 32;
 // Exponent offset and threshold of the running maximum, log2 units.  8 bit: weights
-// up to 2^(7 + 1) use e4m3's range (448) and leave the second piece a floor of
-// 2^-10 / 2^7.  bf16: as in the dense forward.
+// up to 2^(14 + 1) use the range of e5m2 (57344) and of fp16 (65504).  bf16: as in the dense
+// forward.
 template <bool kQ8>
 struct SoftmaxRange {
-  static constexpr float kOffset = kQ8 ? 7.f : 0.f;
+  static constexpr float kOffset = kQ8 ? 14.f : 0.f;
   static constexpr float kThreshold = kQ8 ? 1.f : 8.f;
 };
 
@@ -102,11 +105,12 @@ struct PagedLayout {
   // Slots of one tile each, K and V in turn: K's is free as soon as its scores are there.
   // (K and V in one slot, a wait less, left the loaders too little room: 287 against 259 us.)
   static constexpr int kSlotBytes = kTileBytes;
-  static constexpr int kSlots = kQ8 ? (N == 16 ? 11 : 10) : 6;    // what fits
+  static constexpr int kSlots = kQ8 ? (N == 16 ? 11 : 9) : 6;    // what fits
   static constexpr int kRowBlock = N * 128;      // one 128-byte column block of the N rows
   static constexpr int kOffQ = kSlots * kSlotBytes;  // two e4m3 pieces, or two 64-dim blocks
-  static constexpr int kOffP = kOffQ + 2 * kRowBlock;  // [2 steps][kPer] of two e4m3 pieces, or of bf16
-  static constexpr int kOffBar = kOffP + 4 * kPer * kRowBlock;
+  static constexpr int kOffP = kOffQ + 2 * kRowBlock;  // [2 steps][kPer] of three e5m2 pieces, or of bf16
+  static constexpr int kBlocksP = kQ8 ? 3 : 2;         // row blocks of the weights of one tile
+  static constexpr int kOffBar = kOffP + 2 * kPer * kBlocksP * kRowBlock;
   // kv_full[S], kv_empty[S], q_full, s_full[2], p_full[2], rows_full[R], rows_empty[R], scaled[R]
   static constexpr int kRing = 8;  // tiles that the page lookup may be ahead
   static constexpr int kNumBars = 2 * kSlots + 5 + 3 * kRing;
@@ -120,10 +124,12 @@ struct PagedLayout {
   static constexpr int kOffScales = kOffTile + kRing * 4;
   static constexpr int kSmemBytes = kOffScales + (kQ8 ? kRing * kTile * 16 : 0) + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory of one SM");
-  static constexpr int kCols = kQ8 ? 2 * N : N;  // columns of a product: rows, in 8 bits two pieces of each
+  // columns of the products: rows, in 8 bits as many pieces of each
+  static constexpr int kPiecesQ = kQ8 ? 2 : 1, kPiecesP = kQ8 ? 3 : 1;
+  static constexpr int kCols = kPiecesQ * N, kColsO = kPiecesP * N;
   static constexpr int kColO = 2 * kPer * kCols;  // behind the scores of two steps
   static constexpr uint32_t kTmemCols = (N == 16 ? 64 : 128) * (kQ8 ? 4 : 1);
-  static_assert(kColO + kCols <= (int)kTmemCols, "scores of two steps and O");
+  static_assert(kColO + kColsO <= (int)kTmemCols, "scores of two steps and O");
 };
 
 // rows of one tile that belong to one key head
@@ -256,6 +262,25 @@ __device__ __forceinline__ float2 of_e4m3x2(uint32_t q) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)q, __NV_E4M3)));
 }
 
+// Two fp16 values to the nearest e5m2 pair, and back.
+__device__ __forceinline__ uint32_t to_e5m2x2(__half2 x) {
+  return __nv_cvt_halfraw2_to_fp8x2(__half2_raw(x), __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ __half2 of_e5m2x2(uint32_t q) {
+  const uint32_t x = __byte_perm(q, 0, 0x1404);  // an e5m2 number is the upper byte of an fp16 one
+  return *reinterpret_cast<const __half2*>(&x);
+}
+// Two weights as their three pieces.  Each remainder is an fp16 number, so are 8 times it: exact.
+__device__ __forceinline__ void split_weights(float lo, float hi, uint32_t& q1, uint32_t& q2, uint32_t& q3) {
+  const __half2 eight = __float2half2_rn(8.f);
+  __half2 x = __floats2half2_rn(lo, hi);
+  q1 = to_e5m2x2(x);
+  x = __hmul2(__hsub2(x, of_e5m2x2(q1)), eight);
+  q2 = to_e5m2x2(x);
+  x = __hmul2(__hsub2(x, of_e5m2x2(q2)), eight);
+  q3 = to_e5m2x2(x);
+}
+
 // Lane i < N ends with the sum over the warp of everyone's v[i]; v is used up.
 template <int N>
 __device__ __forceinline__ float warp_sums(float (&v)[N]) {
@@ -276,6 +301,26 @@ __device__ __forceinline__ float warp_sums(float (&v)[N]) {
     }
   }
   return v[0];
+}
+
+// The rows of a product that there are, for this thread's key or dim: kHeads heads' first kLive
+// columns of kHeadRows each, kPieces pieces of them N columns apart, added up, each `step` of
+// the one before it.
+template <int N, int kHeads, int kHeadRows, int kLive, int kPieces>
+__device__ __forceinline__ void ld_rows(uint32_t at, float step, float (&x)[kHeads * kLive]) {
+  constexpr int kRows = kHeads * kLive;
+  uint32_t v[kRows * kPieces];
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) tmem_ld_some<kLive>(at + h * kHeadRows + i * N, v, (i * kHeads + h) * kLive);
+  tmem_ld_done(v);
+#pragma unroll
+  for (int n = 0; n < kRows; ++n) {
+    x[n] = __uint_as_float(v[(kPieces - 1) * kRows + n]);
+#pragma unroll
+    for (int i = kPieces - 2; i >= 0; --i) x[n] = fmaf(x[n], step, __uint_as_float(v[i * kRows + n]));
+  }
 }
 
 // kLive: rows of each key head that there can be, 4 or all of the tile's.  (Four query heads
@@ -434,7 +479,7 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
     // -------------------------------------------------------------------- MMA issuer
     if (elect_one()) {
       constexpr uint32_t kIdescS = kQ8 ? idesc_e4m3_f32(128, 2 * N, false, false) : idesc_bf16_f32(128, N, false, false);
-      constexpr uint32_t kIdescO = kQ8 ? idesc_e4m3_f32(128, 2 * N, true, true) : idesc_bf16_f32(128, N, true, true);
+      constexpr uint32_t kIdescO = kQ8 ? idesc_e4m3_e5m2_f32(128, 3 * N, true, true) : idesc_bf16_f32(128, N, true, true);
       const uint32_t base = smem_u32(smem);
       const SDesc k_desc = sdesc_make(base, 16, 1024);                     // K-major keys
       const SDesc v_desc = sdesc_make(base, kQ8 ? 16 : 16384, 1024);       // dims along M: MN-major
@@ -469,7 +514,7 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
           if (!wait(kv_full + slot, (g / L::kSlots) & 1)) return;
           tc_fence_after();
           const SDesc v = SDesc{v_desc.lo + slot * kSlot16, v_desc.hi};
-          const SDesc pd = SDesc{p_desc.lo + ((x & 1) * L::kPer + u) * 2 * kBlock16, p_desc.hi};
+          const SDesc pd = SDesc{p_desc.lo + ((x & 1) * L::kPer + u) * L::kBlocksP * kBlock16, p_desc.hi};
           // keys 32 i .. or 16 i ..
 #pragma unroll
           for (int i = 0; i < (kQ8 ? 4 : 8); ++i)
@@ -526,19 +571,6 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
     float* wred = factor + 7 * N;    // [4][N] maxima, then sums
     float* wred2 = wred + 4 * N;
     uint32_t c = 0, st = 0;  // tiles and steps so far
-    // the rows of a product, pieces added up
-    auto ld_rows = [&](uint32_t at, float(&x)[kRows]) {
-      constexpr int kPieces = kQ8 ? 2 : 1;
-      uint32_t v[kRows * kPieces];
-#pragma unroll
-      for (int h = 0; h < kHeads; ++h)
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) tmem_ld_some<kLive>(at + h * kHeadRows + i * N, v, (i * kHeads + h) * kLive);
-      tmem_ld_done(v);
-#pragma unroll
-      for (int n = 0; n < kRows; ++n)
-        x[n] = kQ8 ? __uint_as_float(v[n]) + __uint_as_float(v[(kPieces - 1) * kRows + n]) : __uint_as_float(v[n]);
-    };
     // A wait that gives up does not leave at once: the group's barriers need all four
     // warps, so the warp goes on (waiting no more) to the next place where all leave
     // together.
@@ -677,7 +709,7 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
               vinv[u][h] = __uint_as_float((uint32_t)(127 - e) << 23);
             }
           }
-          ld_rows(tmem + lanes + ((st & 1) * L::kPer + u) * L::kCols, y[u]);
+          ld_rows<N, kHeads, kHeadRows, kLive, L::kPiecesQ>(tmem + lanes + ((st & 1) * L::kPer + u) * L::kCols, 1.f, y[u]);
           const int key = key0 + u * kTile;
           const bool masked = key - r + kTile > all_see;
 #pragma unroll
@@ -733,7 +765,7 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
             // columns past the rows there are get whatever alpha holds; they are never read
             uint32_t o[16];
 #pragma unroll 1
-            for (int n0 = 0; n0 < L::kCols; n0 += 16) {
+            for (int n0 = 0; n0 < L::kColsO; n0 += 16) {
               tmem_ld16(tmem + lanes + L::kColO + n0, o);
               tmem_ld_wait16(o);
 #pragma unroll
@@ -749,13 +781,13 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
 #pragma unroll
         for (int u = 0; u < L::kPer; ++u) {
           if (u >= n_tiles) break;
-          const uint32_t pbuf = smem_u32(smem + L::kOffP) + ((st & 1) * L::kPer + u) * 2 * L::kRowBlock + r * 16;
-          // a word of four e4m3 codes, or two words of two bf16 values, for four rows
-          uint32_t p1[N / kGroup][4], p2[N / kGroup][4];
+          const uint32_t pbuf = smem_u32(smem + L::kOffP) + ((st & 1) * L::kPer + u) * L::kBlocksP * L::kRowBlock + r * 16;
+          // a word of four e5m2 codes, or two words of two bf16 values, for four rows
+          uint32_t p1[N / kGroup][4], p2[N / kGroup][4], p3[N / kGroup][4];
 #pragma unroll
           for (int i = 0; i < N / kGroup; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) p1[i][j] = p2[i][j] = 0;
+            for (int j = 0; j < 4; ++j) p1[i][j] = p2[i][j] = p3[i][j] = 0;
 #pragma unroll
           for (int n = 0; n < kRows; n += 4) {
             const int h = n / kLive, x = col(n);
@@ -766,10 +798,12 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
               l[n + j] = fmaf(pw[j], vinv[u][h], l[n + j]);
             }
             if constexpr (kQ8) {
-              const uint32_t lo = to_e4m3x2(pw[0], pw[1]), hi = to_e4m3x2(pw[2], pw[3]);
-              const float2 bl = of_e4m3x2(lo), bh = of_e4m3x2(hi);
-              p1[x / 16][x % 16 / 4] = lo | (hi << 16);
-              p2[x / 16][x % 16 / 4] = to_e4m3x2(pw[0] - bl.x, pw[1] - bl.y) | (to_e4m3x2(pw[2] - bh.x, pw[3] - bh.y) << 16);
+              uint32_t lo[3], hi[3];
+              split_weights(pw[0], pw[1], lo[0], lo[1], lo[2]);
+              split_weights(pw[2], pw[3], hi[0], hi[1], hi[2]);
+              p1[x / 16][x % 16 / 4] = lo[0] | (hi[0] << 16);
+              p2[x / 16][x % 16 / 4] = lo[1] | (hi[1] << 16);
+              p3[x / 16][x % 16 / 4] = lo[2] | (hi[2] << 16);
             } else {
 #pragma unroll
               for (int j = 0; j < 4; j += 2) {
@@ -784,7 +818,10 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
           for (int i = 0; i < N / kGroup; ++i) {
             const uint32_t at = pbuf + i * kTile * 16;
             st_shared_v4(at, p1[i][0], p1[i][1], p1[i][2], p1[i][3]);
-            if constexpr (kQ8) st_shared_v4(at + L::kRowBlock, p2[i][0], p2[i][1], p2[i][2], p2[i][3]);
+            if constexpr (kQ8) {
+              st_shared_v4(at + L::kRowBlock, p2[i][0], p2[i][1], p2[i][2], p2[i][3]);
+              st_shared_v4(at + 2 * L::kRowBlock, p3[i][0], p3[i][1], p3[i][2], p3[i][3]);
+            }
           }
         }
         fence_proxy_async_smem();
@@ -816,7 +853,7 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
       named_bar_sync(1, 128);
       auto sum_of = [&](const float* x, int n) { return (x[n] + x[N + n]) + (x[2 * N + n] + x[3 * N + n]); };
       float o[kRows];
-      ld_rows(tmem + lanes + L::kColO, o);
+      ld_rows<N, kHeads, kHeadRows, kLive, L::kPiecesP>(tmem + lanes + L::kColO, 0.125f, o);
       const bool whole = p.t0 == 0 && p.t1 == p.tiles;
       if (whole) {
 #pragma unroll

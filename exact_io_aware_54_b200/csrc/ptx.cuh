@@ -437,6 +437,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_ma
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The same with e5m2 B (type field 1).
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return idesc_e4m3_f32(M, N, a_mn_major, b_mn_major) | (1u << 10);
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T, 8 bit operands, 32 deep (one thread issues).
 __device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {

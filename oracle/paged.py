@@ -47,17 +47,18 @@ def attend(q, k, v, causal, scale, v_scale=None):
     """One sequence: q [n, Hq, d], k, v [L, Hkv, d] (fp64, dequantised).  Returns o
     [n, Hq, d], lse [n, Hq], and how far a kernel's o and lse may be off:
 
-    * each weight is rounded by at most 2^-8 of itself (bf16, or two e4m3 pieces of
-      2^-4 each), and the sum that divides is that of the rounded weights:
-      2^-8 (sum p |v| + |o|);
-    * with v_scale [L, Hkv] (8 bit), the second piece of a weight w = p * v_scale
-      under 2^-9 of the largest stops at e4m3's subnormal half step, 2^-10 where the
-      largest is at least 2^7: 2^-17 of it;
+    * each weight is rounded by at most 2^-8 of itself (bf16; three e5m2 pieces of an
+      fp16 number: 2^-9 + 2^-11), and the sum that divides is that of the rounded weights
+      (bf16) or of the unrounded ones (pieces): 2^-8 (sum p |v| + |o|) at most;
+    * with v_scale [L, Hkv] (8 bit), the pieces of a weight w = p * v_scale end at an
+      error of 2^-23 + 2^-25 (half of e5m2's subnormal step, the third piece being 64 times
+      up, and of fp16's), where the largest is at least 2^14: 2^-36 of it;
     * 8 bit: an element of q under 2^-9 of its row's largest is off by at most 2^-17
       of that, in either kind the scores' fp32 sums by (d + 2) 2^-24 sum |q k|; a
       score off by t changes o by at most 2 t sum p |v|;
-    * exponentials, sums of n weights and the final logarithm in fp32: (n + 16) 2^-23
-      relative;
+    * exponentials and the final logarithm in fp32, and sums of n weights or products, in
+      which a term passes through no more than n / 16 + 64 additions (a thread or a product takes
+      16 keys or more at a time): (min(n, n / 16 + 48) + 16) 2^-23 relative;
     * o is stored in bf16: 2^-8 |o|.
     """
     n, hq, d = q.shape
@@ -88,11 +89,11 @@ def attend(q, k, v, causal, scale, v_scale=None):
             t = t + scale * 2.0 ** -17 * np.abs(qh[rows]).max(-1) * np.abs(kh).sum(-1).max()
             w = p * v_scale[None, :, g]
             top = w.max(-1, keepdims=True)
-            floor = np.where((w < top * 2.0 ** -8) & seen[rows], top * 2.0 ** -17, 0.0)
+            floor = np.where(seen[rows], top * 2.0 ** -36, 0.0)
             extra = floor @ (np.abs(vh) / v_scale[:, g, None])
         else:
             extra = 0.0
-        t = t + (L + 16) * 2.0 ** -23
+        t = t + (min(L, L / 16 + 48) + 16) * 2.0 ** -23
         o_abs = np.abs(o[rows, h])
         o_tol[rows, h] = 2.0 ** -8 * (a + 2 * o_abs) + extra + 2 * t[:, None] * a + 1e-30
         lse_tol[rows, h] = t + 2.0 ** -22 * np.abs(lse[rows, h]) + 1e-6
