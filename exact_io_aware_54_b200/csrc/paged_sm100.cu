@@ -18,9 +18,9 @@
 //    dim), column = row: a softmax thread owns one key and N scores.
 //  * 8 bit cache without conversion.  K and V tiles stay e4m3 in shared memory and are
 //    multiplied by kind::f8f6f4 MMAs.  The bf16 row of Q is split into two e4m3
-//    pieces, q = q1 + q2: four significant bits each make bf16's eight, exact but
-//    for elements under 2^-9 of the row's largest, off by at most 2^-17 of it (e4m3's
-//    subnormal step).  A weight is an fp16 number cut into three e5m2 pieces (three
+//    pieces, q = q1 + q2 / 32: four significant bits each make bf16's eight, exact but
+//    for elements under 2^-14 of the row's largest, off by at most 2^-22 of it (half of
+//    e4m3's subnormal step, 32 times down).  A weight is an fp16 number cut into three e5m2 pieces (three
 //    significant bits each, e5m2 being the upper byte of fp16), p = p1 + p2 / 8 + p3 / 64,
 //    off by at most 2^-9 + 2^-11 of p, or 2^-36 of the row's largest weight: many weak keys
 //    beside a strong one count as they do in bf16 weights.  (Two e4m3 pieces lose weights
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
                 const float lo = __uint_as_float(x << 16) * up, hi = __uint_as_float(x & 0xFFFF0000u) * up;
                 h1[k] = to_e4m3x2(lo, hi);
                 const float2 back = of_e4m3x2(h1[k]);
-                h2[k] = to_e4m3x2(lo - back.x, hi - back.y);
+                h2[k] = to_e4m3x2((lo - back.x) * 32.f, (hi - back.y) * 32.f);  // at most 8 times 32
               }
               q1[j] = h1[0] | (h1[1] << 16);
               q2[j] = h2[0] | (h2[1] << 16);
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
               vinv[u][h] = __uint_as_float((uint32_t)(127 - e) << 23);
             }
           }
-          ld_rows<N, kHeads, kHeadRows, kLive, L::kPiecesQ>(tmem + lanes + ((st & 1) * L::kPer + u) * L::kCols, 1.f, y[u]);
+          ld_rows<N, kHeads, kHeadRows, kLive, L::kPiecesQ>(tmem + lanes + ((st & 1) * L::kPer + u) * L::kCols, 0.03125f, y[u]);
           const int key = key0 + u * kTile;
           const bool masked = key - r + kTile > all_see;
 #pragma unroll

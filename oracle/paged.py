@@ -53,9 +53,10 @@ def attend(q, k, v, causal, scale, v_scale=None):
     * with v_scale [L, Hkv] (8 bit), the pieces of a weight w = p * v_scale end at an
       error of 2^-23 + 2^-25 (half of e5m2's subnormal step, the third piece being 64 times
       up, and of fp16's), where the largest is at least 2^14: 2^-36 of it;
-    * 8 bit: an element of q under 2^-9 of its row's largest is off by at most 2^-17
-      of that, in either kind the scores' fp32 sums by (d + 2) 2^-24 sum |q k|; a
-      score off by t changes o by at most 2 t sum p |v|;
+    * 8 bit: an element of q under 2^-14 of its row's largest is off by at most 2^-22
+      of that (half of e4m3's subnormal step, 2^-10, in a piece 32 times up, where the
+      largest is at least 2^7), in either kind the scores' fp32 sums by (d + 2) 2^-24
+      sum |q k|; a score off by t changes o by at most 2 t sum p |v|;
     * exponentials and the final logarithm in fp32, and sums of n weights or products, in
       which a term passes through no more than n / 16 + 64 additions (a thread or a product takes
       16 keys or more at a time): (min(n, n / 16 + 48) + 16) 2^-23 relative;
@@ -86,7 +87,7 @@ def attend(q, k, v, causal, scale, v_scale=None):
         a = p @ np.abs(vh)
         t = (d + 2) * 2.0 ** -24 * scale * (np.abs(qh[rows]) @ np.abs(kh).T).max(-1, initial=0)
         if v_scale is not None:
-            t = t + scale * 2.0 ** -17 * np.abs(qh[rows]).max(-1) * np.abs(kh).sum(-1).max()
+            t = t + scale * 2.0 ** -22 * np.abs(qh[rows]).max(-1) * np.abs(kh).sum(-1).max()
             w = p * v_scale[None, :, g]
             top = w.max(-1, keepdims=True)
             floor = np.where(seen[rows], top * 2.0 ** -36, 0.0)

@@ -15,23 +15,14 @@ from tests.test_gpu_paged import Cache, _check, _close
 pytestmark = pytest.mark.gpu
 
 
-def _sink_cache(seed, n, H, d, gap, q8=True, at=5):
-    """One sequence of n keys: against a query of ones, key `at` scores `gap` (within 0.02) and the
-    others within a few tenths of 0; values have a mean of 0.5, key `at`'s are zeros but for one."""
-    c = Cache(seed, [n], H, d, 64, q8)
-    rng = np.random.default_rng(seed)
-    k = 0.25 * rng.standard_normal((n, H, d)) / math.sqrt(d)
-    v = 0.5 + 0.25 * rng.standard_normal((n, H, d))
-    eighths = round(8 * gap * math.sqrt(d))  # shared out over the dims: 8 bit codes hold them exactly
-    k[at] = (eighths // d + (np.arange(d) < eighths % d)) / 8
-    v[at] = 0
-    v[at, :, 1] = 1
-    t = np.arange(n)
-    slots = c.table[0].cpu().numpy()[t // 64], t % 64
+def _fill(c, k, v):
+    """Rows k, v [n, H, d] as the keys and values of a cache's only sequence."""
+    t = np.arange(c.lens[0])
+    slots = c.table[0].cpu().numpy()[t // c.page], t % c.page
     for name, x in (("k", k), ("v", v)):
         x = f64(torch.from_numpy(x).to(torch.bfloat16))
         pages = c.pages[name].cpu()
-        if q8:
+        if c.q8:
             codes, s = paged.quantise(x)
             c.values[name][slots] = paged.dequantise(codes, s)
             pages = pages.view(torch.uint8)
@@ -45,6 +36,20 @@ def _sink_cache(seed, n, H, d, gap, q8=True, at=5):
             pages[slots] = torch.from_numpy(x).to(torch.bfloat16)
         c.pages[name] = pages.cuda()
     return c
+
+
+def _sink_cache(seed, n, H, d, gap, q8=True, at=5):
+    """One sequence of n keys: against a query of ones, key `at` scores `gap` (within 0.02) and the
+    others within a few tenths of 0; values have a mean of 0.5, key `at`'s are zeros but for one."""
+    c = Cache(seed, [n], H, d, 64, q8)
+    rng = np.random.default_rng(seed)
+    k = 0.25 * rng.standard_normal((n, H, d)) / math.sqrt(d)
+    v = 0.5 + 0.25 * rng.standard_normal((n, H, d))
+    eighths = round(8 * gap * math.sqrt(d))  # shared out over the dims: 8 bit codes hold them exactly
+    k[at] = (eighths // d + (np.arange(d) < eighths % d)) / 8
+    v[at] = 0
+    v[at, :, 1] = 1
+    return _fill(c, k, v)
 
 
 COPIES = 150  # sequences that share the pages: whole units in a CTA, not a few tiles each
@@ -83,3 +88,22 @@ def test_weak_keys_of_many_rows():
     """The same over an 8 bit cache by the kernel of many rows."""
     _attend(_sink_cache(310, 16384, 2, 128, 12.0), 4, 20, 311)
     _attend(_sink_cache(310, 16384, 2, 128, 12.0), 4, 16, 312)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("hq,new", [(2, 1), (4, 6), (4, 40)])
+def test_loud_channel_of_the_queries(hq, new, q8, d):
+    """Queries with one channel 2^14 times as loud as the others, which the keys leave empty:
+    the scores are the quiet channels', all of the same sign."""
+    n = 700
+    rng = np.random.default_rng(320)
+    k = rng.uniform(0, 12 / math.sqrt(d), (n, 2, 1)) * np.ones(d)
+    k[..., 3] = 0
+    c = _fill(Cache(321, [n], 2, d, 16, q8), k, rng.standard_normal((n, 2, d)))
+    q = torch.full((new, hq, d), 1.0625, dtype=torch.bfloat16)
+    q[..., 3] = 2.0 ** 14
+    cu = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+    o, lse = fa.fa_fwd_paged(q.cuda(), c.pages["k"], c.pages["v"], cu, c.table, c.seqlens, new, n, True, **c.kw)
+    _check()
+    _close(o, lse.T, c.reference(0, f64(q), True), f"{new} tokens")
