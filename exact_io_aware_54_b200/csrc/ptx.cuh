@@ -539,7 +539,7 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
 // (Cody and Waite range reduction, "Software Manual for the Elementary Functions",
 // 1980, with a polynomial fitted here):
 //   x is clamped to >= -127, so results below 2^-126.5 become +0 (as with
-//   ex2.approx.ftz, and exactly 0 for x = -inf);
+//   ex2.approx.ftz, and exactly 0 for x = -inf; a NaN stays one);
 //   n = rint(x) is read off the fp32 rounding of x + 1.5 * 2^23 (exact for |x| < 2^22);
 //   f = x - n lies in [-1/2, 1/2] and 2^f = c0 + f (c1 + f (c2 + f (c3 + f c4))),
 //   coefficients fitted for the smallest maximum relative error on that interval
@@ -554,9 +554,15 @@ constexpr float kExp2C2 = 0.24024732410907745f;
 constexpr float kExp2C3 = 0.055917903780937195f;
 constexpr float kExp2C4 = 0.009570610709488392f;
 constexpr float kExp2Round = 12582912.0f;  // 1.5 * 2^23
+// Larger of the two, NaN if either is one (fmaxf would return the other).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
 __device__ __forceinline__ float2 exp2_fma2(float2 x) {
-  x.x = fmaxf(x.x, -127.f);
-  x.y = fmaxf(x.y, -127.f);
+  x.x = max_nan(x.x, -127.f);
+  x.y = max_nan(x.y, -127.f);
   const float2 t = fadd2(x, make_float2(kExp2Round, kExp2Round));
   const float2 n = fadd2(t, make_float2(-kExp2Round, -kExp2Round));
   const float2 f = ffma2(n, make_float2(-1.f, -1.f), x);

@@ -399,9 +399,10 @@ FA_API fa_status fa_cache_read(const void* k_pages, const void* v_pages, const u
  * LSE = -inf.  Rows behind the last sequence are left as they were.  Page indices
  * outside the cache are recorded and read as page 0, as in fa_decode_paged; sequences
  * whose offsets do not fit are skipped and recorded.  A sequence's keys and values must
- * be finite: a token that sees an infinity or NaN gets NaN, and so may the sequence's
- * other tokens and, at d = 64, the next key head's (a weight or an element of zero does
- * not remove it).  Rows past a sequence's end may hold anything.
+ * be finite: a token that sees a NaN or scores +inf gets NaN (another infinity may give
+ * what the formula gives), and so may the sequence's other tokens and, at d = 64, the
+ * next key head's (a weight or an element of zero does not remove it).  Rows past a
+ * sequence's end may hold anything.
  * Results do not depend on timing: two calls with the same arguments agree bit for bit.
  */
 FA_API fa_status fa_fwd_paged(const void* q, long long q_row_stride, const void* k_pages, const void* v_pages,
