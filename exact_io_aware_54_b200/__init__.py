@@ -195,7 +195,7 @@ def _paged_workspace(index: int, nbytes) -> torch.Tensor:
     if ws is None:  # as large as any call needs, so that it never has to grow
         ws = torch.zeros(fa_paged_workspace_size(1, 64, 1, 4096, 4096, 128), dtype=torch.uint8,
                          device=torch.device("cuda", index))
-        _paged_ws[key] = ws
+        ws = _paged_ws.setdefault(key, ws)  # another thread's, if that came first
     return ws
 
 
@@ -685,12 +685,13 @@ def _pages_of(k_pages, v_pages, k_scales, v_scales, block_table, B, index):
 
 
 def _paged_ws_of(ws, index, nbytes=lambda: 256):
-    """Pointer and size of the workspace; nbytes() is what the call needs of one of its own."""
+    """The workspace and its size; nbytes() is what the call needs of one of its own.  The
+    caller holds it until its launches are made: it may be the only one that does."""
     if ws is None:
         ws = _paged_workspace(index, nbytes)
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != index or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous CUDA tensor on cuda:{index}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws, ws.numel() * ws.element_size()
 
 
 def fa_cache_write(k, v, k_pages, v_pages, cu_seqlens, block_table, seqlens_k, k_scales=None, v_scales=None,
@@ -712,9 +713,9 @@ def fa_cache_write(k, v, k_pages, v_pages, cu_seqlens, block_table, seqlens_k, k
     vr, v_stride = _rows_of("v", v, total, H, d, index)
     cu = _ptr_of("cu_seqlens", cu_seqlens, _I32, (B + 1,), index)
     lens = _ptr_of("seqlens_k", seqlens_k, _I32, (B,), index)
-    wp, wn = _paged_ws_of(ws, index)
+    ws, wn = _paged_ws_of(ws, index)
     st = lib.fa_cache_write(kr, vr, k_stride, v_stride, cu, table, lens, kp, vp, ks, vs, B, H, total, P, page, most, d,
-                            wp, wn, _raw_stream(index))
+                            ws.data_ptr(), wn, _raw_stream(index))
     _raise("fa_cache_write", st)
 
 
@@ -735,8 +736,8 @@ def fa_cache_read(k_pages, v_pages, cu_seqlens_k, block_table, total_k: int, k_s
     out_v = k_pages.new_empty(shape, dtype=_BF16) if out_v is None else out_v
     ok, ov = _ptr_of("out_k", out_k, _BF16, shape, index), _ptr_of("out_v", out_v, _BF16, shape, index)
     cu = _ptr_of("cu_seqlens_k", cu_seqlens_k, _I32, (B + 1,), index)
-    wp, wn = _paged_ws_of(ws, index)
-    st = lib.fa_cache_read(kp, vp, ks, vs, cu, table, ok, ov, B, H, total_k, P, page, most, d, wp, wn, _raw_stream(index))
+    ws, wn = _paged_ws_of(ws, index)
+    st = lib.fa_cache_read(kp, vp, ks, vs, cu, table, ok, ov, B, H, total_k, P, page, most, d, ws.data_ptr(), wn, _raw_stream(index))
     _raise("fa_cache_read", st)
     return out_k, out_v
 
@@ -770,9 +771,9 @@ def fa_fwd_paged(q, k_pages, v_pages, cu_seqlens_q, block_table, seqlens_k, max_
     op = _ptr_of("out", out, _BF16, (total_q, Hq, d), index)
     lp = _ptr_of("lse", lse, _F32, (Hq, total_q), index)
     max_q, max_k = int(max_seqlen_q), int(max_seqlen_k)
-    wp, wn = _paged_ws_of(ws, index, lambda: lib.fa_paged_workspace_size(B, Hq, Hkv, max_q, max_k, d))
+    ws, wn = _paged_ws_of(ws, index, lambda: lib.fa_paged_workspace_size(B, Hq, Hkv, max_q, max_k, d))
     st = lib.fa_fwd_paged(qp, q_stride, kp, vp, ks, vs, cu, table, lens, op, lp, B, Hq, Hkv, total_q, P, page, most,
-                          max_q, max_k, d, int(bool(causal)), _scale(softmax_scale), wp, wn, _raw_stream(index))
+                          max_q, max_k, d, int(bool(causal)), _scale(softmax_scale), ws.data_ptr(), wn, _raw_stream(index))
     _raise("fa_fwd_paged", st)
     return out, lse
 
@@ -802,9 +803,9 @@ def fa_decode_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq
     lse = q.new_empty((B, Hq), dtype=_F32) if lse is None else lse
     op, lp = _ptr_of("out", out, _BF16, shape, index), _ptr_of("lse", lse, _F32, (B, Hq), index)
     max_k = int(max_seqlen_k)
-    wp, wn = _paged_ws_of(ws, index, lambda: lib.fa_paged_workspace_size(B, Hq, Hkv, 1, max_k, d))
+    ws, wn = _paged_ws_of(ws, index, lambda: lib.fa_paged_workspace_size(B, Hq, Hkv, 1, max_k, d))
     st = lib.fa_decode_paged_q8(qp, kp, vp, ks, vs, table, lens, B, Hq, Hkv, P, page, most, max_k, d,
-                                _scale(softmax_scale), op, lp, wp, wn, _raw_stream(index))
+                                _scale(softmax_scale), op, lp, ws.data_ptr(), wn, _raw_stream(index))
     _raise("fa_decode_paged_q8", st)
     return out, lse
 

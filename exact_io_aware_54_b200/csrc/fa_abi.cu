@@ -750,6 +750,10 @@ static fa_status fwd_paged(const void* q, long long q_row_stride, const void* k_
   a.workspace = workspace;
   a.timeout_ns = wait_timeout_ns();
   a.few_rows = kPagedFewRows;
+  // A call is up to four launches that hand partial states over in the workspace: two host
+  // threads that share a stream and its workspace must not mix theirs.
+  static std::mutex launches;
+  const std::lock_guard<std::mutex> lk(launches);
   // A batch of short and long chunks: each kernel takes its own sequences (the lengths are
   // on the device) and passes over the others.
   const bool some_many = (long long)max_seqlen_q * (Hq / Hkv) > a.few_rows;
