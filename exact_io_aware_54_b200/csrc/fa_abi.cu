@@ -755,9 +755,10 @@ static fa_status fwd_paged(const void* q, long long q_row_stride, const void* k_
   static std::mutex launches;
   const std::lock_guard<std::mutex> lk(launches);
   // A batch of short and long chunks: each kernel takes its own sequences (the lengths are
-  // on the device) and passes over the others.
+  // on the device) and passes over the others.  One kernel for one sequence, whatever its
+  // length, and for single tokens, of which every sequence has as many rows.
   const bool some_many = (long long)max_seqlen_q * (Hq / Hkv) > a.few_rows;
-  if (some_many && B == 1) a.few_rows = 0;  // one sequence: one launch, whatever its length
+  if (some_many && (B == 1 || cu_seqlens_q == nullptr)) a.few_rows = 0;
   if (a.few_rows > 0) {
     const fa_status s = launch_paged_few(a, stream);
     if (s != FA_OK || !some_many) return s;

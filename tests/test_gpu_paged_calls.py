@@ -56,3 +56,40 @@ def test_first_calls_of_two_threads():
     for t in threads:
         t.join()
     assert len(set(got)) == 1
+
+
+def _launched(call):
+    """Names and counts of the library's kernels that a call launches."""
+    import ctypes
+    lib = fa.load()
+    lib.fa_profile_start()
+    call()
+    lib.fa_profile_stop()
+    seen = {}
+    for i in range(lib.fa_profile_count()):
+        name, n, ms = ctypes.c_char_p(), ctypes.c_int(), ctypes.c_double()
+        assert lib.fa_profile_get(i, ctypes.byref(name), ctypes.byref(n), ctypes.byref(ms)) == 0
+        if n.value:
+            seen[name.value.decode()[len("fa_paged_"):]] = n.value
+    return seen
+
+
+FEW, FEW_JOIN, MANY, MANY_JOIN = "kernel", "merge_kernel", "chunk_kernel", "chunk_merge_kernel"
+
+
+@pytest.mark.parametrize("group,keys,kernels", [
+    (32, 300, [FEW, FEW_JOIN]), (33, 300, [MANY, MANY_JOIN]), (40, 128, [MANY]), (65, 129, [MANY, MANY_JOIN]),
+    (32, 128, [FEW])])
+def test_single_tokens_take_one_kernel(group, keys, kernels):
+    """Every sequence has the group's rows, so that one kernel takes them all; units of one tile
+    leave nothing to join."""
+    for lens in ([keys, 7, keys - 1], [keys]):
+        c = Cache(410, lens, 1, 64, 16, True)
+        q = synth._normal((len(lens), group, 64), 411)
+        out = []
+        seen = _launched(lambda: out.extend(fa.fa_decode_paged_q8(
+            q.cuda(), c.pages["k"], c.pages["v"], c.scales["k"], c.scales["v"], c.table, c.seqlens, keys)))
+        _check()
+        assert seen == {k: 1 for k in kernels}
+        for b in range(len(lens)):
+            _close(out[0][b:b + 1], out[1][b:b + 1], c.reference(b, f64(q[b:b + 1]), True), f"sequence {b}")
