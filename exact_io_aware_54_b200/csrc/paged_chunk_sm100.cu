@@ -97,7 +97,7 @@ struct Work {
 __device__ __forceinline__ int keys_of(const PagedArgs& a, const SeqInfo& s, int row) {
   if (!a.causal) return s.lk;
   const int token = min(token_of_row(a, row), s.nq - 1);
-  return max(0, min(s.lk, s.lk - s.nq + token + 1));
+  return max(0, min(s.lk, s.lk0 + token + 1));
 }
 __device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kTile - 1) / kTile); }
 __device__ __forceinline__ int units_of(const PagedArgs& a, int nq) {

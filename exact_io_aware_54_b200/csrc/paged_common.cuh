@@ -66,10 +66,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
-// Sequence b: new tokens, keys and first packed row; nq = -1 when its offsets do not fit,
-// 0 when it is not this kernel's.
+// Sequence b: new tokens (at most max_q of them), keys and first packed row; nq = -1 when its
+// offsets do not fit, 0 when it is not this kernel's.  lk0: how many keys are there before
+// the new tokens (fewer than none when there are more tokens than keys), whether or not all
+// the tokens are attended: token i sees keys 0 .. lk0 + i.
 struct SeqInfo {
-  int nq, lk, qoff;
+  int nq, lk, qoff, lk0;
 };
 __device__ __forceinline__ SeqInfo seq_info(const PagedArgs& a, int b) {
   SeqInfo s;
@@ -77,6 +79,7 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedArgs& a, int b) {
   if (a.cu_q == nullptr) {
     s.nq = 1;
     s.qoff = b;
+    s.lk0 = s.lk - 1;
     return s;
   }
   s.qoff = a.cu_q[b];
@@ -85,6 +88,7 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedArgs& a, int b) {
     s.nq = -1;
     return s;
   }
+  s.lk0 = s.lk - (end - s.qoff);
   s.nq = min(end - s.qoff, a.max_q);
   if (s.nq * a.G < a.min_rows || s.nq * a.G > a.max_rows) s.nq = 0;  // another kernel's
   return s;

@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
         }
         if (tid % kTpr == 0) {
           factor[n] = have ? f : 0.f;
-          limit[n] = (have && a.causal) ? max(0, min(p.s.lk, p.s.lk - p.s.nq + token + 1)) : p.s.lk;
+          limit[n] = (have && a.causal) ? max(0, min(p.s.lk, p.s.lk0 + token + 1)) : p.s.lk;
           thresh[n] = -INFINITY;
           top[n] = -INFINITY;
           ref[n] = -R::kOffset;
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
       named_bar_sync(1, 128);
       // keys that every row of the tile sees: [0, all_see)
       const int first_token = (p.rt * kHeadRows) / a.G;
-      const int all_see = a.causal ? max(0, min(p.s.lk, p.s.lk - p.s.nq + first_token + 1)) : p.s.lk;
+      const int all_see = a.causal ? max(0, min(p.s.lk, p.s.lk0 + first_token + 1)) : p.s.lk;
 
       float l[kRows], lr[kQ8 ? 1 : kRows];
 #pragma unroll

@@ -389,8 +389,9 @@ FA_API fa_status fa_cache_read(const void* k_pages, const void* v_pages, const u
  *   causal       : bottom-right aligned per sequence: token i sees keys
  *                  0 .. seqlens_k[b] - n_b + i; else all seqlens_k[b] keys
  *   seqlens_k    : device int32 [B], clamped to [0, max_seqlen_k]
- *   max_seqlen_q, max_seqlen_k : upper bounds of n_b and of the lengths (longer chunks
- *                  are cut to it); max_seqlen_k must not exceed
+ *   max_seqlen_q, max_seqlen_k : upper bounds of n_b and of the lengths (of a longer chunk
+ *                  the first max_seqlen_q tokens are attended, each to its own keys, and
+ *                  the others' rows left as they were); max_seqlen_k must not exceed
  *                  max_pages_per_seq * page_size (FA_ERR_INVALID_ARG)
  *   o            : [total_q, Hq, d] bf16 (written), contiguous
  *   lse          : [Hq, total_q] fp32 (written)

@@ -93,3 +93,25 @@ def test_single_tokens_take_one_kernel(group, keys, kernels):
         assert seen == {k: 1 for k in kernels}
         for b in range(len(lens)):
             _close(out[0][b:b + 1], out[1][b:b + 1], c.reference(b, f64(q[b:b + 1]), True), f"sequence {b}")
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("most", [1, 6, 130])
+def test_chunks_longer_than_their_bound(most, causal, d, q8):
+    """The first tokens are attended as what they are, the first of the chunk; the others' rows stay."""
+    new, lens = [most + 7, 3, most + 200, most], [most + 40, 60, most + 90, 700]  # the third: tokens that see nothing
+    c = Cache(420, lens, 2, d, 16, q8)
+    cu = synth.cu_seqlens_of(new)
+    q = synth._normal((sum(new), 4, d), 421)
+    o = torch.full((sum(new), 4, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, sum(new)), 7.0, device="cuda")
+    fa.fa_fwd_paged(q.cuda(), c.pages["k"], c.pages["v"], cu.cuda(), c.table, c.seqlens, most, max(lens), causal, out=o,
+                    lse=lse, **c.kw)
+    _check()
+    for b, n in enumerate(new):
+        at, cut = int(cu[b]), min(n, most)
+        ref = [x[:cut] for x in c.reference(b, f64(q[at:at + n]), causal)]
+        _close(o[at:at + cut], lse[:, at:at + cut].T, ref, f"sequence {b}, {cut} of {n}")
+        assert (o[at + cut:at + n] == 7).all() and (lse[:, at + cut:at + n] == 7).all()
