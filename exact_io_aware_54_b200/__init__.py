@@ -613,7 +613,8 @@ def fa_decode_paged(q, k_pages, v_pages, block_table, seqlens_k, max_seqlen_k: i
 # --------------------------------------------------------------------------- paged cache
 #
 # A serving step makes these calls once per layer, so their checks are written to cost
-# little: each tensor is looked at once, and compared by device index.
+# little: each tensor is looked at once, and compared by device index.  A call without a
+# row (a step in which no sequence has a new token) has nothing to do and makes no launch.
 
 _BF16, _FP8, _U8, _I32, _F32 = torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.float32
 
@@ -713,6 +714,8 @@ def fa_cache_write(k, v, k_pages, v_pages, cu_seqlens, block_table, seqlens_k, k
     vr, v_stride = _rows_of("v", v, total, H, d, index)
     cu = _ptr_of("cu_seqlens", cu_seqlens, _I32, (B + 1,), index)
     lens = _ptr_of("seqlens_k", seqlens_k, _I32, (B,), index)
+    if total == 0:
+        return
     ws, wn = _paged_ws_of(ws, index)
     st = lib.fa_cache_write(kr, vr, k_stride, v_stride, cu, table, lens, kp, vp, ks, vs, B, H, total, P, page, most, d,
                             ws.data_ptr(), wn, _raw_stream(index))
@@ -736,6 +739,8 @@ def fa_cache_read(k_pages, v_pages, cu_seqlens_k, block_table, total_k: int, k_s
     out_v = k_pages.new_empty(shape, dtype=_BF16) if out_v is None else out_v
     ok, ov = _ptr_of("out_k", out_k, _BF16, shape, index), _ptr_of("out_v", out_v, _BF16, shape, index)
     cu = _ptr_of("cu_seqlens_k", cu_seqlens_k, _I32, (B + 1,), index)
+    if total_k == 0:
+        return out_k, out_v
     ws, wn = _paged_ws_of(ws, index)
     st = lib.fa_cache_read(kp, vp, ks, vs, cu, table, ok, ov, B, H, total_k, P, page, most, d, ws.data_ptr(), wn, _raw_stream(index))
     _raise("fa_cache_read", st)
@@ -770,6 +775,8 @@ def fa_fwd_paged(q, k_pages, v_pages, cu_seqlens_q, block_table, seqlens_k, max_
     lse = q.new_empty((Hq, total_q), dtype=_F32) if lse is None else lse
     op = _ptr_of("out", out, _BF16, (total_q, Hq, d), index)
     lp = _ptr_of("lse", lse, _F32, (Hq, total_q), index)
+    if total_q == 0:
+        return out, lse
     max_q, max_k = int(max_seqlen_q), int(max_seqlen_k)
     ws, wn = _paged_ws_of(ws, index, lambda: lib.fa_paged_workspace_size(B, Hq, Hkv, max_q, max_k, d))
     st = lib.fa_fwd_paged(qp, q_stride, kp, vp, ks, vs, cu, table, lens, op, lp, B, Hq, Hkv, total_q, P, page, most,
@@ -802,6 +809,8 @@ def fa_decode_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq
     out = torch.empty_like(q) if out is None else out
     lse = q.new_empty((B, Hq), dtype=_F32) if lse is None else lse
     op, lp = _ptr_of("out", out, _BF16, shape, index), _ptr_of("lse", lse, _F32, (B, Hq), index)
+    if B == 0:
+        return out, lse
     max_k = int(max_seqlen_k)
     ws, wn = _paged_ws_of(ws, index, lambda: lib.fa_paged_workspace_size(B, Hq, Hkv, 1, max_k, d))
     st = lib.fa_decode_paged_q8(qp, kp, vp, ks, vs, table, lens, B, Hq, Hkv, P, page, most, max_k, d,

@@ -343,7 +343,8 @@ FA_API fa_status fa_decode_paged(const void* q, const void* k_pages, const void*
  * d in {64, 128}; num_pages * page_size and max_pages_per_seq * page_size < 2^31.
  * The k, v and q arguments of fa_cache_write and fa_fwd_paged are rows [total, H, d]
  * with *_row_stride elements between rows (>= H * d, a multiple of 8), so a slice of a
- * fused projection needs no copy.
+ * fused projection needs no copy.  These calls want at least one sequence and one row
+ * (FA_ERR_INVALID_ARG; a caller with none has nothing to call for).
  */
 
 /*

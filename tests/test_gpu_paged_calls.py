@@ -115,3 +115,32 @@ def test_chunks_longer_than_their_bound(most, causal, d, q8):
         ref = [x[:cut] for x in c.reference(b, f64(q[at:at + n]), causal)]
         _close(o[at:at + cut], lse[:, at:at + cut].T, ref, f"sequence {b}, {cut} of {n}")
         assert (o[at + cut:at + n] == 7).all() and (lse[:, at + cut:at + n] == 7).all()
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_calls_without_a_row(q8):
+    """Steps in which no sequence has a token, or a key, and a batch of no sequence."""
+    H, d = 2, 64
+    c = Cache(430, [20, 0], H, d, 16, q8)
+    before = {x: c.pages[x].view(torch.uint8).clone() for x in "kv"}
+    zeros = torch.zeros(3, dtype=torch.int32, device="cuda")
+    rows = torch.empty((0, H, d), dtype=torch.bfloat16, device="cuda")
+
+    def calls():
+        fa.fa_cache_write(rows, rows, c.pages["k"], c.pages["v"], zeros, c.table, c.seqlens, **c.kw)
+        k, v = fa.fa_cache_read(c.pages["k"], c.pages["v"], zeros, c.table, 0, **c.kw)
+        assert k.shape == v.shape == (0, H, d) and k.dtype == torch.bfloat16
+        q = torch.empty((0, 4, d), dtype=torch.bfloat16, device="cuda")
+        for most in (0, 5):
+            o, lse = fa.fa_fwd_paged(q, c.pages["k"], c.pages["v"], zeros, c.table, c.seqlens, most, 20, True, **c.kw)
+            assert o.shape == q.shape and lse.shape == (4, 0)
+        if q8:
+            o, lse = fa.fa_decode_paged_q8(q, c.pages["k"], c.pages["v"], c.scales["k"], c.scales["v"], c.table[:0],
+                                           c.seqlens[:0], 0)
+            assert o.shape == q.shape and lse.shape == (0, 4)
+
+    assert _launched(calls) == {}
+    _check()
+    assert all(torch.equal(c.pages[x].view(torch.uint8), before[x]) for x in "kv")
+    with pytest.raises(ValueError):  # a wrong shape is one with no row too
+        fa.fa_cache_write(rows[:, :1], rows, c.pages["k"], c.pages["v"], zeros, c.table, c.seqlens, **c.kw)
