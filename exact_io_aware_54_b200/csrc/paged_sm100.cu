@@ -859,10 +859,11 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
 #pragma unroll
         for (int n = 0; n < kRows; ++n) {
           const float sum = sum_of(wred2, n);
-          const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+          const float inv = sum > 0.f ? 1.f / sum : sum;
+          const float x = sum == 0.f ? 0.f : o[n] * inv;  // every key hidden: O = 0, whatever V holds
           const int row = out_row[col(n)];
           const bool mine = D == 128 || n / kLive == r / 64;  // a pair's head has its half of O^T
-          if (row >= 0 && mine) a.o[(size_t)row * D + (D == 64 ? (r & 63) : r)] = __float2bfloat16(o[n] * inv);
+          if (row >= 0 && mine) a.o[(size_t)row * D + (D == 64 ? (r & 63) : r)] = __float2bfloat16(x);
         }
         if (tid < kRows && out_row[col(tid)] >= 0) {
           const float sum = sum_of(wred, tid);

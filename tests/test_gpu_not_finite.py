@@ -34,6 +34,24 @@ def test_nan_key_of_a_cache(n, d, q8):
         assert o[:, mine].isnan().all() and lse[mine].isnan().all(), f"key {at}"
 
 
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [9, 15, 200])
+def test_tokens_that_see_nothing_beside_nan(n, d, q8):
+    """More tokens than keys, all values NaN: the first tokens see none of them."""
+    L = 4
+    c = Cache(155, [L, L], 2, d, 16, q8)
+    c.pages["v"].view(torch.uint8).fill_(0xFF)
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    q = synth._normal((2 * n, 4, d), 156).cuda()
+    o, lse = fa.fa_fwd_paged(q, c.pages["k"], c.pages["v"], cu, c.table, c.seqlens, n, L, True, **c.kw)
+    _check()
+    for b in range(2):
+        none = slice(b * n, b * n + n - L)
+        assert (o[none] == 0).all() and (lse[:, none] == -math.inf).all()
+        assert o[b * n + n - L:b * n + n].isnan().all()
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("n", [2, 150])
 def test_infinite_score_over_a_cache(n, d):
