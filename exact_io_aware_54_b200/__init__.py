@@ -685,6 +685,14 @@ def _pages_of(k_pages, v_pages, k_scales, v_scales, block_table, B, index):
     return shape, most, kp, vp, ks, vs, _ptr_of("block_table", block_table, _I32, (B, most), index)
 
 
+def _bound(name, n):
+    """A length bound as the C calls take it (a larger int would lose its upper bits there)."""
+    n = int(n)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {n}")
+    return n
+
+
 def _paged_ws_of(ws, index, nbytes=lambda: 256):
     """The workspace and its size; nbytes() is what the call needs of one of its own.  The
     caller holds it until its launches are made: it may be the only one that does."""
@@ -777,7 +785,7 @@ def fa_fwd_paged(q, k_pages, v_pages, cu_seqlens_q, block_table, seqlens_k, max_
     lp = _ptr_of("lse", lse, _F32, (Hq, total_q), index)
     if total_q == 0:
         return out, lse
-    max_q, max_k = int(max_seqlen_q), int(max_seqlen_k)
+    max_q, max_k = _bound("max_seqlen_q", max_seqlen_q), _bound("max_seqlen_k", max_seqlen_k)
     ws, wn = _paged_ws_of(ws, index, lambda: lib.fa_paged_workspace_size(B, Hq, Hkv, max_q, max_k, d))
     st = lib.fa_fwd_paged(qp, q_stride, kp, vp, ks, vs, cu, table, lens, op, lp, B, Hq, Hkv, total_q, P, page, most,
                           max_q, max_k, d, int(bool(causal)), _scale(softmax_scale), ws.data_ptr(), wn, _raw_stream(index))
@@ -811,7 +819,7 @@ def fa_decode_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq
     op, lp = _ptr_of("out", out, _BF16, shape, index), _ptr_of("lse", lse, _F32, (B, Hq), index)
     if B == 0:
         return out, lse
-    max_k = int(max_seqlen_k)
+    max_k = _bound("max_seqlen_k", max_seqlen_k)
     ws, wn = _paged_ws_of(ws, index, lambda: lib.fa_paged_workspace_size(B, Hq, Hkv, 1, max_k, d))
     st = lib.fa_decode_paged_q8(qp, kp, vp, ks, vs, table, lens, B, Hq, Hkv, P, page, most, max_k, d,
                                 _scale(softmax_scale), op, lp, ws.data_ptr(), wn, _raw_stream(index))

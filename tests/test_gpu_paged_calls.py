@@ -144,3 +144,16 @@ def test_calls_without_a_row(q8):
     assert all(torch.equal(c.pages[x].view(torch.uint8), before[x]) for x in "kv")
     with pytest.raises(ValueError):  # a wrong shape is one with no row too
         fa.fa_cache_write(rows[:, :1], rows, c.pages["k"], c.pages["v"], zeros, c.table, c.seqlens, **c.kw)
+
+
+def test_bounds_past_32_bits_are_refused():
+    """2^32 + 20 is not a bound of 20."""
+    c = Cache(440, [40], 2, 64, 16, True)
+    q = synth._normal((1, 2, 64), 441).cuda()
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    for big in (2 ** 32, 2 ** 32 + 20, 2 ** 63 + 1, -2 ** 32 + 20):
+        for most in (dict(max_seqlen_q=1, max_seqlen_k=big), dict(max_seqlen_q=big, max_seqlen_k=40)):
+            with pytest.raises(ValueError, match="32 bits"):
+                fa.fa_fwd_paged(q, c.pages["k"], c.pages["v"], cu, c.table, c.seqlens, **most, **c.kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            fa.fa_decode_paged_q8(q, c.pages["k"], c.pages["v"], c.scales["k"], c.scales["v"], c.table, c.seqlens, big)
