@@ -179,22 +179,36 @@ def paged_workspace(device=None, nbytes: int = 0) -> torch.Tensor:
     when they are given none; pass it to :func:`fa_check` after them.
 
     One per stream, since two calls that may run at the same time must not share a
-    workspace.  Calls under stream capture get one of their own from the graph's
-    memory, so that graphs share it neither with each other nor with eager calls."""
+    workspace.  Under stream capture this makes a new one (cleared in every replay) from
+    the graph's memory: hand it to the captured calls as ``ws`` and keep it, and fa_check
+    reads their status after a replay.  Captured calls that are given none each take
+    memory of the graph's, so that graphs share it neither with each other nor with eager
+    calls; their status cannot be read."""
     index = torch.device(device).index if device is not None else None
-    return _paged_workspace(torch.cuda.current_device() if index is None else index, lambda: nbytes)
+    index = torch.cuda.current_device() if index is None else index
+    if torch.cuda.is_current_stream_capturing():
+        ws = _new_paged_workspace(max(int(nbytes), _paged_ws_bytes()), index)
+        ws[:256].zero_()  # the status word; the rest is written before it is read
+        return ws
+    return _paged_workspace(index, lambda: nbytes)
+
+
+def _paged_ws_bytes() -> int:
+    """As much as any call needs."""
+    return fa_paged_workspace_size(1, 64, 1, 4096, 4096, 128)
+
+
+def _new_paged_workspace(nbytes: int, index: int) -> torch.Tensor:
+    return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
 
 
 def _paged_workspace(index: int, nbytes) -> torch.Tensor:
-    if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(max(int(nbytes()), 256), dtype=torch.uint8, device=torch.device("cuda", index))
-        ws[:256].zero_()  # the status word; the rest is written before it is read
-        return ws
+    if torch.cuda.is_current_stream_capturing():  # (nobody can read its status word, which is not cleared)
+        return _new_paged_workspace(max(int(nbytes()), 256), index)
     key = (index, _raw_stream(index))
     ws = _paged_ws.get(key)
     if ws is None:  # as large as any call needs, so that it never has to grow
-        ws = torch.zeros(fa_paged_workspace_size(1, 64, 1, 4096, 4096, 128), dtype=torch.uint8,
-                         device=torch.device("cuda", index))
+        ws = _new_paged_workspace(_paged_ws_bytes(), index).zero_()
         ws = _paged_ws.setdefault(key, ws)  # another thread's, if that came first
     return ws
 

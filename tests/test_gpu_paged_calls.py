@@ -157,3 +157,70 @@ def test_bounds_past_32_bits_are_refused():
                 fa.fa_fwd_paged(q, c.pages["k"], c.pages["v"], cu, c.table, c.seqlens, **most, **c.kw)
         with pytest.raises(ValueError, match="32 bits"):
             fa.fa_decode_paged_q8(q, c.pages["k"], c.pages["v"], c.scales["k"], c.scales["v"], c.table, c.seqlens, big)
+
+
+def _captured(call):
+    """A graph of the call, what it returned, and the types of the graph's nodes."""
+    from cuda.bindings import runtime
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        out = call()
+    raw = runtime.cudaGraph_t(init_value=g.raw_cuda_graph())
+    err, _, n = runtime.cudaGraphGetNodes(raw)
+    assert err == runtime.cudaError_t.cudaSuccess
+    err, nodes, n = runtime.cudaGraphGetNodes(raw, n)
+    assert err == runtime.cudaError_t.cudaSuccess
+    types = [runtime.cudaGraphNodeGetType(node)[1] for node in nodes[:n]]
+    g.instantiate()
+    return g, out, [t.name for t in types]
+
+
+@pytest.mark.parametrize("new,kernels", [(1, 2), (40, 4)])
+def test_captured_calls_are_their_kernels(new, kernels):
+    """No other node: the kernels start early behind one another."""
+    c = Cache(450, [500, 300], 2, 128, 16, True)
+    cu = torch.tensor([0, new, 2 * new], dtype=torch.int32, device="cuda")
+    q, x = (synth._normal((2 * new, h, 128), 451 + h).cuda() for h in (8, 2))
+
+    def call():
+        fa.fa_cache_write(x, x, c.pages["k"], c.pages["v"], cu, c.table, c.seqlens, **c.kw)
+        return fa.fa_fwd_paged(q, c.pages["k"], c.pages["v"], cu, c.table, c.seqlens, new, 500, True, **c.kw)
+
+    want = call()  # (also the one-time set-up, which a capture must not meet first)
+    g, out, types = _captured(call)
+    assert types == ["cudaGraphNodeTypeKernel"] * (1 + kernels)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    del g
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_status_of_captured_calls(new):
+    """With a workspace made under the capture: recorded in each replay, and cleared by the next."""
+    c = Cache(460, [500, 300], 2, 128, 16, True)
+    cu = torch.tensor([0, new, 2 * new], dtype=torch.int32, device="cuda")
+    q = synth._normal((2 * new, 8, 128), 461).cuda()
+    table = c.table.clone()
+
+    def call():
+        ws = fa.paged_workspace()
+        return ws, fa.fa_fwd_paged(q, c.pages["k"], c.pages["v"], cu, table, c.seqlens, new, 500, True, ws=ws, **c.kw)
+
+    want = fa.fa_fwd_paged(q, c.pages["k"], c.pages["v"], cu, table, c.seqlens, new, 500, True, **c.kw)
+    g, (ws, out), _ = _captured(call)
+    for bad in (False, True, False):
+        table.copy_(c.table)
+        if bad:
+            table[0, 3] = -1
+        g.replay()
+        assert fa.fa_check(ws) == (INVALID if bad else 0)
+        assert bad or torch.equal(out[0], want[0])
+    table[0, 3] = -1
+    g.replay()
+    table.copy_(c.table)
+    g.replay()  # cleared, and nothing to record
+    assert fa.fa_check(ws) == 0
+    _check()
+    del g
