@@ -79,7 +79,10 @@ class PerDeviceOnce {
     if (done_[dev].load(std::memory_order_acquire)) return true;
     std::lock_guard<std::mutex> lk(mu_);
     if (done_[dev].load(std::memory_order_relaxed)) return true;
-    if (!set()) return false;
+    if (!set()) {
+      cudaGetLastError();  // consumed
+      return false;
+    }
     done_[dev].store(true, std::memory_order_release);
     return true;
   }

@@ -223,7 +223,8 @@ inline cudaError_t launch_dependent(void (*kernel)(const PagedArgs), dim3 grid, 
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
-  return err == cudaSuccess ? cudaGetLastError() : err;
+  const cudaError_t last = cudaGetLastError();  // consumed, or the next launch would report it
+  return err != cudaSuccess ? err : last;
 }
 
 inline PagedArgs paged_args(const PagedLaunch& L) {

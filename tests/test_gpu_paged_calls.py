@@ -224,3 +224,53 @@ def test_status_of_captured_calls(new):
     assert fa.fa_check(ws) == 0
     _check()
     del g
+
+
+FAILED_LAUNCH = """
+import ctypes, sys, torch
+sys.path.insert(0, ".")
+from cuda.bindings import runtime as rt
+import exact_io_aware_54_b200 as fa
+
+new = int(sys.argv[1])
+bf16 = dict(dtype=torch.bfloat16, device="cuda")
+pages, q, x = torch.zeros((4, 16, 1, 64), **bf16), torch.zeros((new, 1, 64), **bf16), torch.zeros((new, 1, 64), **bf16)
+table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+cu, lens = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, new], [64]))
+ws, o, lse = fa.paged_workspace(), torch.empty_like(q), torch.empty((1, new), device="cuda")
+torch.cuda.synchronize()
+lib, p = fa.load(), lambda t: t.data_ptr()
+
+def attend(stream):
+    return lib.fa_fwd_paged(p(q), 64, p(pages), p(pages), None, None, p(cu), p(table), p(lens), p(o), p(lse), 1, 1, 1,
+                            new, 4, 16, 4, new, 64, 64, 1, 0.0, p(ws), ws.numel(), stream)
+
+def write(stream):
+    return lib.fa_cache_write(p(x), p(x), 64, 64, p(cu), p(table), p(lens), p(pages), p(pages), None, None, 1, 1, new, 4,
+                              16, 4, 64, p(ws), ws.numel(), stream)
+
+assert attend(0) == 0 and write(0) == 0
+torch.cuda.synchronize()
+err, stream = rt.cudaStreamCreateWithFlags(rt.cudaStreamNonBlocking)
+assert err == 0
+assert rt.cudaStreamBeginCapture(stream, rt.cudaStreamCaptureMode.cudaStreamCaptureModeThreadLocal)[0] == 0
+assert rt.cudaStreamSynchronize(stream)[0] != 0  # not allowed: the capture is now invalid, and so is a launch into it
+cuda_error = [k for k, v in fa.STATUS.items() if v == "FA_ERR_CUDA"][0]
+assert attend(int(stream)) == cuda_error
+assert rt.cudaStreamEndCapture(stream)[0] != 0
+assert write(0) == 0, "an earlier call's error"
+assert attend(0) == 0 and fa.fa_check(ws) == 0
+print("fine")
+"""
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_error_of_a_launch_is_reported_once(new):
+    """A launch into a capture that has become invalid fails on the host; the next call is not blamed for it."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FAILED_LAUNCH, str(new)], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert run.stdout.strip() == "fine", run.stderr[-2000:]
