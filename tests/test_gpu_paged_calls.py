@@ -274,3 +274,63 @@ def test_error_of_a_launch_is_reported_once(new):
     run = subprocess.run([sys.executable, "-c", FAILED_LAUNCH, str(new)], cwd=root, capture_output=True, text=True,
                          timeout=300)
     assert run.stdout.strip() == "fine", run.stderr[-2000:]
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,lens,group,kernels", [
+    ([8, 8], [300, 40], 4, [FEW, FEW_JOIN]),  # 32 rows a key head
+    ([11, 11], [300, 40], 3, [FEW, FEW_JOIN, MANY, MANY_JOIN]),  # 33: the bound says so, whatever the lengths
+    ([8, 1], [128, 128], 4, [FEW]),  # one tile of keys: nothing to join
+    ([8, 1], [129, 128], 4, [FEW, FEW_JOIN]),
+    ([90, 1], [128, 20], 4, [FEW, MANY]),  # a short chunk and a long one
+    ([90, 1], [129, 20], 4, [FEW, FEW_JOIN, MANY, MANY_JOIN]),
+    ([3], [700], 4, [FEW, FEW_JOIN]),
+    ([90], [700], 4, [MANY, MANY_JOIN]),  # one sequence: one kernel
+    ([90], [90], 4, [MANY])])
+def test_kernels_of_a_chunk(new, lens, group, kernels, d, q8):
+    c = Cache(470, lens, 2, d, 16, q8)
+    cu = synth.cu_seqlens_of(new)
+    q = synth._normal((sum(new), 2 * group, d), 471)
+    out = []
+    seen = _launched(lambda: out.extend(fa.fa_fwd_paged(q.cuda(), c.pages["k"], c.pages["v"], cu.cuda(), c.table, c.seqlens,
+                                                        max(new), max(lens), True, **c.kw)))
+    _check()
+    assert seen == {k: 1 for k in kernels}
+    for b, n in enumerate(new):
+        sl = slice(int(cu[b]), int(cu[b]) + n)
+        _close(out[0][sl], out[1][:, sl].T, c.reference(b, f64(q[sl]), True), f"sequence {b}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_single_sequence_with_a_large_bound(d):
+    """A bound of many rows and a chunk of one: the kernel of many rows."""
+    c = Cache(480, [300], 2, d, 16, True)
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    q = synth._normal((1, 4, d), 481)
+    out = []
+    seen = _launched(lambda: out.extend(fa.fa_fwd_paged(q.cuda(), c.pages["k"], c.pages["v"], cu, c.table, c.seqlens, 512,
+                                                        300, True, **c.kw)))
+    _check()
+    assert seen == {MANY: 1, MANY_JOIN: 1}
+    _close(out[0], out[1].T, c.reference(0, f64(q), True), "one token")
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("hkv", [4, 2])
+def test_chunk_and_packed_forward_within_their_tolerances(hkv, q8):
+    """The same keys read back and given to the packed forward: apart by no more than what both may
+    be off (its roundings are the reference's: bf16 weights, the rounded sum, bf16 outputs)."""
+    lens, new = [1500, 40, 513], [150, 7, 200]
+    c = Cache(490, lens, hkv, 128, 16, q8)
+    q = synth._normal((sum(new), 4, 128), 491)
+    cu, cuk = synth.cu_seqlens_of(new), synth.cu_seqlens_of(lens).cuda()
+    o, _ = fa.fa_fwd_paged(q.cuda(), c.pages["k"], c.pages["v"], cu.cuda(), c.table, c.seqlens, 200, 1500, True, **c.kw)
+    k, v = fa.fa_cache_read(c.pages["k"], c.pages["v"], cuk, c.table, sum(lens), **c.kw)
+    k, v = (x.repeat_interleave(4 // hkv, 1).contiguous() for x in (k, v))
+    o2, _ = fa.fa_fwd_varlen(q.cuda(), k, v, cu.cuda(), cuk, 200, 1500, causal=True)
+    _check()
+    for b, n in enumerate(new):
+        sl = slice(int(cu[b]), int(cu[b]) + n)
+        tol = c.reference(b, f64(q[sl]), True)[2]
+        assert (abs(f64(o[sl]) - f64(o2[sl])) <= 2 * tol).all()
