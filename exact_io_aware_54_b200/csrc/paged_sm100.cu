@@ -262,23 +262,24 @@ __device__ __forceinline__ float2 of_e4m3x2(uint32_t q) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)q, __NV_E4M3)));
 }
 
-// Two fp16 values to the nearest e5m2 pair, and back.
-__device__ __forceinline__ uint32_t to_e5m2x2(__half2 x) {
-  return __nv_cvt_halfraw2_to_fp8x2(__half2_raw(x), __NV_SATFINITE, __NV_E5M2);
-}
-__device__ __forceinline__ __half2 of_e5m2x2(uint32_t q) {
-  const uint32_t x = __byte_perm(q, 0, 0x1404);  // an e5m2 number is the upper byte of an fp16 one
-  return *reinterpret_cast<const __half2*>(&x);
-}
-// Two weights as their three pieces.  Each remainder is an fp16 number, so are 8 times it: exact.
-__device__ __forceinline__ void split_weights(float lo, float hi, uint32_t& q1, uint32_t& q2, uint32_t& q3) {
+// Four weights as the bytes of their three e5m2 pieces.  An e5m2 number is the upper byte of an
+// fp16 one, so the nearest (ties away from zero) is that of its bits + 0x80, up to 57344, and
+// the remainder is an fp16 number, as is 8 times it.  A NaN may come out as anything: it is in
+// the sum that divides.
+__device__ __forceinline__ void split_weights(const float (&w)[4], uint32_t& p1, uint32_t& p2, uint32_t& p3) {
   const __half2 eight = __float2half2_rn(8.f);
-  __half2 x = __floats2half2_rn(lo, hi);
-  q1 = to_e5m2x2(x);
-  x = __hmul2(__hsub2(x, of_e5m2x2(q1)), eight);
-  q2 = to_e5m2x2(x);
-  x = __hmul2(__hsub2(x, of_e5m2x2(q2)), eight);
-  q3 = to_e5m2x2(x);
+  __half2 lo = __floats2half2_rn(w[0], w[1]), hi = __floats2half2_rn(w[2], w[3]);
+  auto piece = [&](uint32_t& codes) {
+    uint32_t a = *reinterpret_cast<const uint32_t*>(&lo) + 0x00800080u, b = *reinterpret_cast<const uint32_t*>(&hi) + 0x00800080u;
+    codes = __byte_perm(a, b, 0x7531);
+    a &= 0xFF00FF00u;
+    b &= 0xFF00FF00u;
+    lo = __hmul2(__hsub2(lo, *reinterpret_cast<const __half2*>(&a)), eight);
+    hi = __hmul2(__hsub2(hi, *reinterpret_cast<const __half2*>(&b)), eight);
+  };
+  piece(p1);
+  piece(p2);
+  piece(p3);
 }
 
 // Lane i < N ends with the sum over the warp of everyone's v[i]; v is used up.
@@ -798,12 +799,8 @@ __global__ void __launch_bounds__(kThreads<N, kQ8>, 1)
               l[n + j] = fmaf(pw[j], vinv[u][h], l[n + j]);
             }
             if constexpr (kQ8) {
-              uint32_t lo[3], hi[3];
-              split_weights(pw[0], pw[1], lo[0], lo[1], lo[2]);
-              split_weights(pw[2], pw[3], hi[0], hi[1], hi[2]);
-              p1[x / 16][x % 16 / 4] = lo[0] | (hi[0] << 16);
-              p2[x / 16][x % 16 / 4] = lo[1] | (hi[1] << 16);
-              p3[x / 16][x % 16 / 4] = lo[2] | (hi[2] << 16);
+              const int i = x / 16, j = x % 16 / 4;
+              split_weights(pw, p1[i][j], p2[i][j], p3[i][j]);
             } else {
 #pragma unroll
               for (int j = 0; j < 4; j += 2) {

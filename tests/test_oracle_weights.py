@@ -10,7 +10,8 @@ from oracle import paged
 def three_pieces(p):
     """p as the 8 bit kernel holds it: three e5m2 pieces, 8 and 64 times up for the later two."""
     h = torch.from_numpy(p).to(torch.float16)
-    e5 = lambda x: x.to(torch.float8_e5m2).to(torch.float16)
+    # the upper byte of the fp16 number, to the nearest (ties away from zero)
+    e5 = lambda x: ((x.view(torch.int16).int() + 0x80) & 0xFF00).to(torch.int16).view(torch.float16)
     a = e5(h)
     r = (h - a) * 8
     b = e5(r)
