@@ -687,8 +687,11 @@ static bool paged_sizes_ok(int B, int Hq, int Hkv, int max_seqlen_q, int max_seq
 
 // Rows per key head up to which a sequence goes to the few-row kernel: one tile of its 32 (d =
 // 64, where two heads share a tile: two).  16 sequences of 4000 keys, no groups, there and in
-// the chunk kernel: 32 heads of 128, 32 tokens 174 and 245 us (bf16), 259 and 354 (8 bit), 40
-// tokens 331 and 244, 490 and 355; 16 heads of 64, 32 tokens 92 and 113, 138 and 140.
+// the chunk kernel, device time: 32 heads of 128, 32 tokens 173 and 252 us (bf16), 284 and 350
+// (8 bit), 40 tokens 324 and 247, 544 and 351; 16 heads of 64, 16 tokens 53 and 115 (bf16), 79
+// and 138 (8 bit), 32 tokens 92 and 113, 148 and 138, 40 tokens 131 and 115, 221 and 139.  One
+// bound for all costs 64-wide heads in 8 bits 7% between 17 and 32 rows, and spares batches of
+// short chunks the second pair of launches.
 constexpr int kPagedFewRows = 32;
 
 size_t fa_paged_workspace_size(int B, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int d) {

@@ -21,12 +21,15 @@
 //    parts, one per CTA (one CTA per SM).  A unit cut by a border leaves fp32 partial
 //    states of its 256 rows, two at most per CTA, which a second kernel joins in order.
 //    512 tokens over 16K keys (8 key heads, G = 4) are 64 units for 148 CTAs.
-//  * What it measures: 8192 causal tokens over themselves (32 heads of 128, bf16) 620 us, 886
-//    TFLOP/s: the chain from scores to weights to the next scores bounds it, as it does the
-//    dense forward (3600 of a tile's 4360 cycles; the products take 2100).  16 ragged
-//    sequences of 64-wide heads 141 us.  512 tokens over 16K keys (8 key heads), 8 bit:
-//    203 us, where the conversion of the tiles by the loader warps bounds it (6000 cycles a
-//    tile).
+//  * Weights are rounded to bf16, the tensor cores' operand, and O is divided by the sum of
+//    the rounded ones, as in the dense forward; lse comes from the unrounded sum.
+//  * What it measures: 8192 causal tokens over themselves (32 heads of 128, bf16) 630 to
+//    660 us inside a graph, by the clock under the power limit, and 690 as a call: 790 to 870
+//    TFLOP/s.  The chain from scores to weights to the next scores bounds it, as it does the
+//    dense forward (3600 of a tile's 4360 cycles; the products take 2100), which takes 575 us
+//    for the same work.  16 ragged sequences of 64-wide heads 150 us a call.  512 tokens
+//    over 16K keys (8 key heads), 8 bit: 204 us, where the conversion of the tiles by the
+//    loader warps bounds it (6000 cycles a tile); of 64-wide heads 147 us.
 //  * Warp roles (512 threads): 0 MMA issuer, 1 page lookup, 4-7 loaders (8 bits, d = 128:
 //    2-7), 8-11 and 12-15 the softmax groups of the two row tiles.
 #include "paged_common.cuh"

@@ -61,11 +61,14 @@
 //  * Every role is a small loop: one warp of each runs per scheduler, and with the loaders'
 //    loops unrolled (2000 instructions each) two fifths of all stalls were for instructions
 //    not yet fetched (64 requests, 8 key heads: 499 us; 272 with small loops over a ring of rows).
-//  * What it measures: 64 requests of 512 to 16384 keys, 32 query and 8 key heads of 128, 8
-//    bit: 224 us, 85% of the measured copy rate; bound by the softmax and MMA chain of a tile,
-//    which takes about as long as its bytes.  One sequence of 8192 keys, 32 heads: 22.5 us for
-//    10 us of bytes, the rest the start (four dependent loads, lengths, page, keys, and the
-//    first scores: 5.5 us), the epilogue and the join (1 and 3 us).
+//  * What it measures (device time): 64 requests of 512 to 16384 keys, 32 query and 8 key
+//    heads of 128, 8 bit: 225 us, 85% of the measured copy rate; bound by the softmax and MMA
+//    chain of a tile, which takes about as long as its bytes.  Four tokens each: 318 us, bound
+//    by the softmax of 16 rows a key, each weight cut into its pieces (two e4m3 pieces with one
+//    scale took 284).  Over a bf16 cache 361 us, at the measured copy rate.  One sequence of
+//    8192 keys, 32 heads, 8 bit: 21.5 us for 10 us of bytes, the rest the start (four
+//    dependent loads, lengths, page, keys, and the first scores: 5.5 us), the epilogue and the
+//    join (1 and 3 us).
 //  * Few waits: the issue order Q K^T of step s + 1, then P V of step s, makes the scores'
 //    barrier of a step imply that the products of two steps before have read their
 //    weights, and the weights' barrier that the scores have been read; the barrier that
@@ -81,7 +84,7 @@ namespace {
 // Loader warps, half of them for K.  One warp each takes about 1050 cycles for a tile of 8
 // bit keys, as long as its bytes do: two are never ahead (eight: 234 us for 64 requests, four
 // 228).  With 32 rows the 8 bit softmax takes longer and needs the registers: 32 tokens, 16 x
-// 4000 keys, 32 heads of 128, with two and four 259 and 289 us, in bf16 177 and 174.
+// 4000 keys, 32 heads of 128, with two and four 287 and 320 us, in bf16 177 and 174.
 template <int N, bool kQ8>
 constexpr int kLoaders = kQ8 && N == 32 ? 2 : 4;
 template <int N, bool kQ8>
