@@ -179,7 +179,8 @@ def paged_workspace(device=None, nbytes: int = 0) -> torch.Tensor:
     when they are given none; pass it to :func:`fa_check` after them.
 
     One per stream, since two calls that may run at the same time must not share a
-    workspace.  Under stream capture this makes a new one (cleared in every replay) from
+    workspace; as large as any call needs (39 MB on a B200) and kept, whatever `nbytes`
+    says, so that its status word stays where it is.  Under stream capture this makes a new one (cleared in every replay) from
     the graph's memory: hand it to the captured calls as ``ws`` and keep it, and fa_check
     reads their status after a replay.  Captured calls that are given none each take
     memory of the graph's, so that graphs share it neither with each other nor with eager

@@ -535,6 +535,13 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   return d;
 }
 
+// Larger of the two, NaN if either is one (fmaxf would return the other).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // 2^x for two values on the FMA and integer pipes, leaving the MUFU unit free
 // (Cody and Waite range reduction, "Software Manual for the Elementary Functions",
 // 1980, with a polynomial fitted here):
@@ -554,12 +561,6 @@ constexpr float kExp2C2 = 0.24024732410907745f;
 constexpr float kExp2C3 = 0.055917903780937195f;
 constexpr float kExp2C4 = 0.009570610709488392f;
 constexpr float kExp2Round = 12582912.0f;  // 1.5 * 2^23
-// Larger of the two, NaN if either is one (fmaxf would return the other).
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float m;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
-  return m;
-}
 __device__ __forceinline__ float2 exp2_fma2(float2 x) {
   x.x = max_nan(x.x, -127.f);
   x.y = max_nan(x.y, -127.f);

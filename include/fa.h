@@ -428,7 +428,8 @@ FA_API fa_status fa_decode_paged_q8(const void* q, const void* k_pages, const vo
 /*
  * Workspace of fa_fwd_paged and fa_decode_paged_q8 (max_seqlen_q = 1) in bytes, 0 when
  * the arguments are invalid.  Only its first 256 bytes need to be zero before the first
- * use.
+ * use.  Calls on one stream may share it, from several host threads too (a call's
+ * launches are made under a lock); calls that may run at the same time may not.
  */
 FA_API size_t fa_paged_workspace_size(int B, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int d);
 
